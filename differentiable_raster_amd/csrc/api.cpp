@@ -28,6 +28,22 @@ gs_status fail(gs_status s, const char* fmt, ...) {
     return s;
 }
 
+}  // namespace
+
+gs_status gsmi::api_fail(gs_status s, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    g_last_error = buf;
+    return s;
+}
+
+void gsmi::api_clear() { g_last_error.clear(); }
+
+namespace {
+
 gs_status hip_check(hipError_t e, const char* what) {
     if (e == hipSuccess) return GS_OK;
     return fail(GS_ERR_HIP, "%s: %s", what, hipGetErrorString(e));

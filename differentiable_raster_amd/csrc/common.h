@@ -59,6 +59,10 @@ __device__ __forceinline__ float one_minus_alpha(float o, float G, float v, floa
     return v <= amax ? fmaf(-o, G, 1.0f) : 1.0f - amax;
 }
 
+// The thread's error message (gs_last_error), for the API files other than api.cpp.
+gs_status api_fail(gs_status s, const char* fmt, ...);
+void api_clear();
+
 // ---------------------------------------------------------------------------------------
 // Launchers (defined next to their kernels).
 // ---------------------------------------------------------------------------------------

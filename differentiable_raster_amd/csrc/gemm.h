@@ -1,0 +1,534 @@
+// The tiled matrix product of the neural decoder and the product of a few rows, as templates;
+// gemm_bf16.hip, gemm_f16.hip and gemm_e4m3.hip instantiate them.
+//
+//   acc[i][j] = sum_k a[i][k] b[j][k],  then the epilogue (bias, activation, residual, gate product, derivative).
+//
+// Both operands of the matrix instruction take 8 consecutive k of one row per lane, and the order of k
+// within a step is free as long as both sides agree.  An operand whose rows lie along k ("kRowK") is read
+// from LDS in 16-byte chunks; one whose rows lie along its free axis ("kRowFree": the weights and the
+// gradients of a backward product) keeps that layout in LDS and is read through the transposing LDS read,
+// so no product needs a transposed copy in memory.
+// The result's j runs along the four accumulator registers of a lane (b is the instruction's first
+// operand), so a lane stores four neighbours of a row at once.
+#pragma once
+
+#include "elem.h"
+#include "neural.h"
+
+namespace gsmi {
+namespace gemm {
+
+struct TBf16 {
+    static constexpr int type = GS_TYPE_BF16, chunk = 8;
+    static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    }
+};
+struct TF16 {
+    static constexpr int type = GS_TYPE_F16, chunk = 8;
+    static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    }
+};
+// 16 values per chunk: two instructions, each taking half of the chunk of both operands.
+struct TE4m3 {
+    static constexpr int type = GS_TYPE_E4M3, chunk = 16;
+    static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+        const long a0 = (long)((uint64_t)a[0] | (uint64_t)a[1] << 32), a1 = (long)((uint64_t)a[2] | (uint64_t)a[3] << 32);
+        const long b0 = (long)((uint64_t)b[0] | (uint64_t)b[1] << 32), b1 = (long)((uint64_t)b[2] | (uint64_t)b[3] << 32);
+        c = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(a0, b0, c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(a1, b1, c, 0, 0, 0);
+    }
+};
+
+// ---------------------------------------------------------------------------------------------------
+// Epilogue: four neighbours along j of row i.
+// ---------------------------------------------------------------------------------------------------
+__device__ __forceinline__ void epi_store(const Epi& e, int32_t i, int32_t j, int32_t J, f32x4 v) {
+    const int64_t at = (int64_t)i * e.y_si + (int64_t)j * e.y_sj;
+    const int32_t end = e.y_pad > J ? e.y_pad : J;
+    if (e.y_sj == 1 && (e.y_si & 3) == 0 && j + 4 <= end && (reinterpret_cast<uintptr_t>(e.y) & 15) == 0) {
+        for (int k = 0; k < 4; k++)
+            if (j + k >= J) v[k] = 0.0f;
+        store_elem4(e.y, e.y_type, at, v);
+    } else {
+        for (int k = 0; k < 4; k++)
+            if (j + k < end) store_elem(e.y, e.y_type, at + k * e.y_sj, j + k < J ? v[k] : 0.0f);
+    }
+}
+
+__device__ __forceinline__ f32x4 epi_load(const void* p, int type, int64_t si, int64_t sj, int32_t i, int32_t j, int32_t J) {
+    const int64_t at = (int64_t)i * si + (int64_t)j * sj;
+    if (sj == 1 && (si & 3) == 0 && j + 4 <= J && (reinterpret_cast<uintptr_t>(p) & 15) == 0) return load_elem4(p, type, at);
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k = 0; k < 4; k++)
+        if (j + k < J) v[k] = load_elem(p, type, at + k * sj);
+    return v;
+}
+
+// The scaled sum with its bias; `row` is j's row in b (the gated kinds have the ups at J + j).
+__device__ __forceinline__ f32x4 epi_pre(const Epi& e, f32x4 acc, int32_t i, int32_t j, int32_t J, int32_t shift) {
+    f32x4 v = acc;
+    if (e.scale_i) {
+        const float si = e.scale_i[i];
+        for (int k = 0; k < 4; k++) v[k] *= si * e.scale_j[shift + (j + k < J ? j + k : J - 1)];
+    }
+    if (e.bias) {
+        if (e.bias_on_i) {
+            const float b = e.bias[i];
+            for (int k = 0; k < 4; k++) v[k] += b;
+        } else {
+            for (int k = 0; k < 4; k++) v[k] += e.bias[shift + (j + k < J ? j + k : J - 1)];
+        }
+    }
+    return v;
+}
+
+__device__ __forceinline__ void epi_linear(const Epi& e, f32x4 acc, int32_t i, int32_t j, int32_t J) {
+    f32x4 v = epi_pre(e, acc, i, j, J, 0);
+    if (e.act != GS_ACT_NONE)
+        for (int k = 0; k < 4; k++) v[k] = act_value(v[k], e.act);
+    if (e.res) v += epi_load(e.res, e.y_type, e.r_si, e.r_sj, i, j, J);
+    epi_store(e, i, j, J, v);
+}
+__device__ __forceinline__ void epi_gated(const Epi& e, f32x4 gate, f32x4 up, int32_t i, int32_t j, int32_t J) {
+    const f32x4 g = epi_pre(e, gate, i, j, J, 0), u = epi_pre(e, up, i, j, J, J);
+    f32x4 v;
+    for (int k = 0; k < 4; k++) v[k] = act_value(g[k], e.act) * u[k];
+    epi_store(e, i, j, J, v);
+}
+// dz = dy act'(z); returned for the column sums.
+__device__ __forceinline__ f32x4 epi_dz(const Epi& e, f32x4 acc, int32_t i, int32_t j, int32_t J) {
+    const f32x4 z = epi_pre(e, acc, i, j, J, 0), dy = epi_load(e.dy, e.dy_type, e.d_si, e.d_sj, i, j, J);
+    f32x4 o;
+    for (int k = 0; k < 4; k++) {
+        float v, d;
+        act_both(z[k], e.act, v, d);
+        o[k] = j + k < J ? dy[k] * d : 0.0f;
+    }
+    epi_store(e, i, j, J, o);
+    return o;
+}
+// Gradients of the gate and the up, stored at columns j and J + j.
+__device__ __forceinline__ void epi_dgated(const Epi& e, f32x4 gate, f32x4 up, int32_t i, int32_t j, int32_t J, f32x4& dg, f32x4& du) {
+    const f32x4 g = epi_pre(e, gate, i, j, J, 0), u = epi_pre(e, up, i, j, J, J);
+    const f32x4 dh = epi_load(e.dy, e.dy_type, e.d_si, e.d_sj, i, j, J);
+    for (int k = 0; k < 4; k++) {
+        float v, d;
+        act_both(g[k], e.act, v, d);
+        const bool in = j + k < J;
+        dg[k] = in ? dh[k] * u[k] * d : 0.0f;
+        du[k] = in ? dh[k] * v : 0.0f;
+    }
+    Epi f = e;
+    f.y_pad = 0;
+    epi_store(f, i, j, J, dg);
+    // the ups' columns, with the padding of the whole row after the last of them
+    const int64_t at = (int64_t)i * e.y_si;
+    const int32_t end = e.y_pad > 2 * J ? e.y_pad : 2 * J;
+    if ((J & 3) == 0 && (e.y_si & 3) == 0 && j + 4 <= J && (reinterpret_cast<uintptr_t>(e.y) & 15) == 0) {
+        store_elem4(e.y, e.y_type, at + J + j, du);
+    } else {
+        for (int k = 0; k < 4; k++)
+            if (j + k < J) store_elem(e.y, e.y_type, at + J + j + k, du[k]);
+    }
+    if (j + 4 >= J)
+        for (int32_t c = 2 * J; c < end; c++) store_elem(e.y, e.y_type, at + c, 0.0f);
+}
+
+// ---------------------------------------------------------------------------------------------------
+// Loads of a tile: 16-byte chunks through a buffer descriptor whose range ends with the operand, so a
+// chunk outside of it reads zeros.
+// ---------------------------------------------------------------------------------------------------
+__device__ __forceinline__ u32x4 buffer_chunk(const void* base, int32_t bytes, int32_t off) {
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00020000);
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+constexpr int32_t kOutside = 0x7FFFFFF0;  // past every range
+
+// swizzle of a kRowFree tile: the 32-byte granule of k row k, see read_free()
+template <int ROWS>
+__device__ __forceinline__ int free_swizzle(int k) {
+    return ROWS >= 128 ? (k & 3) | ((k >> 3) & 1) << 2 : ((k >> 1) & 1) | ((k >> 3) & 1) << 1;
+}
+
+// ROWS free rows x 128 bytes of k (kRowK), or 64 k x ROWS free columns (kRowFree), by THREADS threads.
+template <class T, int ROWS, int THREADS, int LAYOUT, bool PAIRED, int TJ>
+struct Operand {
+    static constexpr int N = ROWS * 8 / THREADS;  // chunks per thread
+    static_assert(ROWS * 8 % THREADS == 0 && (LAYOUT == kRowK || T::chunk == 8), "");
+    static constexpr int ES = 16 / T::chunk;      // bytes of an element
+    static constexpr int BK = kStepBytes / ES;    // k per step
+    int32_t off[N];   // byte offsets from the step's base
+    int32_t lds[N];   // byte offsets in the tile
+    int32_t first_k[N];
+
+    __device__ __forceinline__ void init(int tid, int64_t ld, int32_t pair_rows) {
+#pragma unroll
+        for (int n = 0; n < N; n++) {
+            const int id = tid + n * THREADS;
+            if (LAYOUT == kRowK) {
+                const int row = id >> 3, c = id & 7;
+                int64_t src = row;
+                if (PAIRED) {  // rows of a wave's strip: first half gates, second half ups
+                    const int w = row / TJ, rr = row % TJ, half = rr / (TJ / 2);
+                    src = (int64_t)half * pair_rows + w * (TJ / 2) + rr % (TJ / 2);
+                }
+                off[n] = (int32_t)(src * ld * ES + c * 16);
+                lds[n] = row * 128 + ((c ^ (row & 7)) << 4);
+                first_k[n] = c * T::chunk;
+            } else {
+                const int k = id / (ROWS / 8), c = id % (ROWS / 8);
+                off[n] = (int32_t)(k * ld * ES + c * 16);
+                lds[n] = k * ROWS * 2 + (((c >> 1) ^ free_swizzle<ROWS>(k)) << 5) + ((c & 1) << 4);
+                first_k[n] = k;
+            }
+        }
+    }
+    // p: first element of the tile's free rows at k = 0; rows: free rows from there to the operand's end
+    // (kRowK: at most what the tile reads; kRowFree: columns); left: k from the step's first to the end.
+    __device__ __forceinline__ void load(u32x4 (&r)[N], const char* p, int64_t ld, int64_t k0, int32_t rows, int64_t left) const {
+        const bool whole = left >= BK;
+        const int32_t l = whole ? BK : (int32_t)left;
+        const char* base = LAYOUT == kRowK ? p + k0 * ES : p + k0 * ld * ES;
+        // a row along k ends with whole chunks: the operand is padded with zeros where k does not
+        const int32_t lp = (l + T::chunk - 1) / T::chunk * T::chunk;
+        const int32_t bytes = LAYOUT == kRowK ? (int32_t)(((int64_t)(rows - 1) * ld + lp) * ES)
+                                              : (int32_t)(((int64_t)(l - 1) * ld + rows) * ES);
+#pragma unroll
+        for (int n = 0; n < N; n++) r[n] = buffer_chunk(base, bytes, whole || first_k[n] < l ? off[n] : kOutside);
+    }
+    __device__ __forceinline__ void store(const u32x4 (&r)[N], char* tile) const {
+#pragma unroll
+        for (int n = 0; n < N; n++) *reinterpret_cast<u32x4*>(tile + lds[n]) = r[n];
+    }
+};
+
+// 16 rows from row0 on, chunk step kk (0 or 1) of a kRowK tile: lane (l & 15) its row, (l >> 4) its 8 k.
+__device__ __forceinline__ u32x4 read_k(const char* tile, int row0, int kk, int lane) {
+    const int row = row0 + (lane & 15), c = kk * 4 + (lane >> 4);
+    return *reinterpret_cast<const u32x4*>(tile + row * 128 + ((c ^ (row & 7)) << 4));
+}
+// The same fragment of a kRowFree tile.  One transposing read serves 16 lanes: lane l gives the address of
+// four columns of k row l / 4 and receives column l % 16 of four k rows.  The 32-byte granules of the k rows
+// that one instruction touches are spread over the banks by free_swizzle().
+template <int ROWS>
+__device__ __forceinline__ u32x4 read_free(const char* tile, int row0, int kk, int lane) {
+    const int l = lane & 15, k = kk * 32 + (lane >> 4) * 8 + (l >> 2);
+    const char* p = tile + k * ROWS * 2 + (((row0 >> 4) ^ free_swizzle<ROWS>(k)) << 5) + ((l & 3) << 3);
+    // k and k + 4 (k % 8 < 4) have the same swizzle
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * ROWS * 2));
+    const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
+    return u32x4{a[0], a[1], b[0], b[1]};
+}
+
+// Workgroup -> tile: workgroups go round the 8 XCDs, so each XCD takes a contiguous run of tiles, and a
+// run walks strips of 8 i-tiles, so that the tiles of one XCD at a time share operands in its L2.
+__device__ __forceinline__ void tile_of(int32_t id, int32_t ni, int32_t nj, int32_t& ti, int32_t& tj) {
+    const int32_t n = ni * nj, q = n >> 3, r = n & 7, x = id & 7;
+    const int32_t m = x * q + (x < r ? x : r) + (id >> 3);
+    constexpr int32_t kStrip = 8;
+    const int32_t strip = m / (kStrip * nj), first = strip * kStrip;
+    const int32_t h = ni - first < kStrip ? ni - first : kStrip, in = m - strip * kStrip * nj;
+    ti = first + in % h;
+    tj = in / h;
+}
+
+template <class T, int SHAPE, int LA, int LB, int EPI>
+__global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(GemmArgs g) {
+    constexpr int BI = kTileDims[SHAPE].bi, BJ = kTileDims[SHAPE].bj, WI = kTileDims[SHAPE].wi;
+    constexpr int THREADS = SHAPE == kTile256 ? 512 : 256, WJ = THREADS / 64 / WI;
+    constexpr int TI = BI / WI, TJ = BJ / WJ, FI = TI / 16, FJ = TJ / 16;
+    constexpr bool PAIRED = EPI == kEpiGated || EPI == kEpiDGated;
+    constexpr int BK = kStepBytes / (16 / T::chunk);
+    constexpr int A_BYTES = BI * 128, B_BYTES = BJ * 128;
+    __shared__ __align__(1024) char smem[2 * (A_BYTES + B_BYTES)];
+    typedef Operand<T, BI, THREADS, LA, false, TI> OpA;
+    typedef Operand<T, BJ, THREADS, LB, PAIRED, TJ> OpB;
+    constexpr int ES = OpA::ES;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wi = wave / WJ, wj = wave % WJ;
+    constexpr int BJO = PAIRED ? BJ / 2 : BJ;  // result columns of a tile
+    const int32_t ni = (g.I + BI - 1) / BI, nj = (g.J + BJO - 1) / BJO;
+    int32_t ti, tj;
+    tile_of(blockIdx.x, ni, nj, ti, tj);
+    const int32_t i0 = ti * BI, j0 = tj * BJO;
+
+    const char* pa = static_cast<const char*>(g.a) + (LA == kRowK ? (int64_t)i0 * g.lda : (int64_t)i0) * ES;
+    const char* pb = static_cast<const char*>(g.b) + (LB == kRowK ? (int64_t)j0 * g.ldb : (int64_t)j0) * ES;
+    // rows (columns) of the operands inside the tile's reach; the paired b reaches to the end of the ups
+    const int32_t ra = LA == kRowK ? (g.I - i0 < BI ? g.I - i0 : BI) : g.a_cols - i0;
+    const int32_t rb = PAIRED ? 2 * g.J - j0 : (LB == kRowK ? (g.J - j0 < BJ ? g.J - j0 : BJ) : g.b_cols - j0);
+    OpA oa;
+    OpB ob;
+    oa.init(tid, g.lda, 0);
+    ob.init(tid, g.ldb, g.J);
+
+    const int64_t kt0 = (int64_t)blockIdx.z * g.kt_per_split;
+    const int64_t kt_all = (g.K + BK - 1) / BK;
+    const int64_t kt1 = kt0 + g.kt_per_split < kt_all ? kt0 + g.kt_per_split : kt_all;
+
+    f32x4 acc[FI][FJ];
+#pragma unroll
+    for (int i = 0; i < FI; i++)
+#pragma unroll
+        for (int j = 0; j < FJ; j++) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    u32x4 va[OpA::N], vb[OpB::N];
+    if (kt0 < kt1) {
+        oa.load(va, pa, g.lda, kt0 * BK, ra, g.K - kt0 * BK);
+        ob.load(vb, pb, g.ldb, kt0 * BK, rb, g.K - kt0 * BK);
+        oa.store(va, smem);
+        ob.store(vb, smem + A_BYTES);
+    }
+    __syncthreads();
+    int cur = 0;
+    for (int64_t kt = kt0; kt < kt1; kt++) {
+        const bool more = kt + 1 < kt1;
+        if (more) {
+            oa.load(va, pa, g.lda, (kt + 1) * BK, ra, g.K - (kt + 1) * BK);
+            ob.load(vb, pb, g.ldb, (kt + 1) * BK, rb, g.K - (kt + 1) * BK);
+        }
+        const char* ta = smem + cur * (A_BYTES + B_BYTES);
+        const char* tb = ta + A_BYTES;
+#pragma unroll
+        for (int kk = 0; kk < 2; kk++) {
+            u32x4 fa[FI], fb[FJ];
+#pragma unroll
+            for (int i = 0; i < FI; i++)
+                fa[i] = LA == kRowK ? read_k(ta, wi * TI + i * 16, kk, lane) : read_free<BI>(ta, wi * TI + i * 16, kk, lane);
+#pragma unroll
+            for (int j = 0; j < FJ; j++)
+                fb[j] = LB == kRowK ? read_k(tb, wj * TJ + j * 16, kk, lane) : read_free<BJ>(tb, wj * TJ + j * 16, kk, lane);
+#pragma unroll
+            for (int i = 0; i < FI; i++)
+#pragma unroll
+                for (int j = 0; j < FJ; j++) acc[i][j] = T::mma(fb[j], fa[i], acc[i][j]);
+        }
+        if (more) {
+            char* nt = smem + (cur ^ 1) * (A_BYTES + B_BYTES);
+            oa.store(va, nt);
+            ob.store(vb, nt + A_BYTES);
+        }
+        __syncthreads();
+        cur ^= 1;
+    }
+
+    // lane: row i = lane & 15 of a 16x16 block, columns (lane >> 4) * 4 + 0..3
+    const int32_t il = i0 + wi * TI + (lane & 15), jl = (lane >> 4) * 4;
+    if (EPI == kEpiLinear) {
+#pragma unroll
+        for (int i = 0; i < FI; i++)
+#pragma unroll
+            for (int j = 0; j < FJ; j++) {
+                const int32_t ii = il + i * 16, jj = j0 + wj * TJ + j * 16 + jl;
+                if (g.partial) {
+                    float* o = g.partial + ((int64_t)blockIdx.z * g.I + ii) * g.J + jj;
+                    for (int k = 0; k < 4; k++)
+                        if (ii < g.I && jj + k < g.J) o[k] = acc[i][j][k];
+                } else if (ii < g.I && jj < g.J) {
+                    epi_linear(g.e, acc[i][j], ii, jj, g.J);
+                }
+            }
+    } else if (EPI == kEpiGated) {
+#pragma unroll
+        for (int i = 0; i < FI; i++)
+#pragma unroll
+            for (int j = 0; j < FJ / 2; j++) {
+                const int32_t ii = il + i * 16, jj = j0 + wj * (TJ / 2) + j * 16 + jl;
+                if (ii < g.I && jj < g.J) epi_gated(g.e, acc[i][j], acc[i][j + FJ / 2], ii, jj, g.J);
+            }
+    } else {
+        constexpr int NJ = EPI == kEpiDGated ? FJ / 2 : FJ;
+        const int64_t strip = (int64_t)ti * WI + wi;
+#pragma unroll
+        for (int j = 0; j < NJ; j++) {
+            const int32_t jj = j0 + wj * (NJ * 16) + j * 16 + jl;
+            f32x4 s0 = {0.0f, 0.0f, 0.0f, 0.0f}, s1 = s0;
+            const int32_t reach = EPI == kEpiDz && g.e.y_pad > g.J ? g.e.y_pad : g.J;
+#pragma unroll
+            for (int i = 0; i < FI; i++) {
+                const int32_t ii = il + i * 16;
+                if (ii < g.I && jj < reach) {
+                    if (EPI == kEpiDz) {
+                        s0 += epi_dz(g.e, acc[i][j], ii, jj, g.J);
+                    } else {
+                        f32x4 dg, du;
+                        epi_dgated(g.e, acc[i][j], acc[i][j + FJ / 2], ii, jj, g.J, dg, du);
+                        s0 += dg;
+                        s1 += du;
+                    }
+                }
+            }
+            if (g.e.colsum) {
+#pragma unroll
+                for (int m = 1; m < 16; m <<= 1)
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        s0[k] += __shfl_xor(s0[k], m);
+                        if (EPI == kEpiDGated) s1[k] += __shfl_xor(s1[k], m);
+                    }
+                if ((lane & 15) == 0) {
+                    const int64_t cols = EPI == kEpiDGated ? 2 * (int64_t)g.J : g.J;
+                    for (int k = 0; k < 4; k++)
+                        if (jj + k < g.J) {
+                            g.e.colsum[strip * cols + jj + k] = s0[k];
+                            if (EPI == kEpiDGated) g.e.colsum[strip * cols + g.J + jj + k] = s1[k];
+                        }
+                }
+            }
+        }
+    }
+}
+
+template <class T, int SHAPE, int LA, int LB, int EPI>
+hipError_t launch_one(const GemmArgs& g, hipStream_t s) {
+    constexpr bool PAIRED = EPI == kEpiGated || EPI == kEpiDGated;
+    const int64_t bj = PAIRED ? kTileDims[SHAPE].bj / 2 : kTileDims[SHAPE].bj;
+    const int64_t tiles = ((g.I + (int64_t)kTileDims[SHAPE].bi - 1) / kTileDims[SHAPE].bi) * ((g.J + bj - 1) / bj);
+    hipLaunchKernelGGL((gemm_kernel<T, SHAPE, LA, LB, EPI>), dim3((unsigned)tiles, 1, (unsigned)g.splits),
+                       dim3(SHAPE == kTile256 ? 512 : 256), 0, s, g);
+    return hipGetLastError();
+}
+
+template <class T, int SHAPE>
+hipError_t launch_shape(Layout la, Layout lb, EpiKind kind, const GemmArgs& g, hipStream_t s) {
+    if (la == kRowK && lb == kRowK) {
+        if (kind == kEpiLinear) return launch_one<T, SHAPE, kRowK, kRowK, kEpiLinear>(g, s);
+        if (kind == kEpiGated) return launch_one<T, SHAPE, kRowK, kRowK, kEpiGated>(g, s);
+        if constexpr (T::chunk == 8) {
+            if (kind == kEpiDz) return launch_one<T, SHAPE, kRowK, kRowK, kEpiDz>(g, s);
+            return launch_one<T, SHAPE, kRowK, kRowK, kEpiDGated>(g, s);
+        }
+    }
+    if constexpr (T::chunk == 8) {
+        if (kind == kEpiLinear && lb == kRowFree) {
+            if (la == kRowK) return launch_one<T, SHAPE, kRowK, kRowFree, kEpiLinear>(g, s);
+            return launch_one<T, SHAPE, kRowFree, kRowFree, kEpiLinear>(g, s);
+        }
+    }
+    return hipErrorInvalidValue;
+}
+
+template <class T>
+hipError_t launch_type(TileShape shape, Layout la, Layout lb, EpiKind kind, const GemmArgs& g, hipStream_t s) {
+    switch (shape) {
+        case kTile256: return launch_shape<T, kTile256>(la, lb, kind, g, s);
+        case kTile128: return launch_shape<T, kTile128>(la, lb, kind, g, s);
+        case kTile64: return launch_shape<T, kTile64>(la, lb, kind, g, s);
+        case kTile64x256: return launch_shape<T, kTile64x256>(la, lb, kind, g, s);
+        case kTile256x64: return launch_shape<T, kTile256x64>(la, lb, kind, g, s);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+// ---------------------------------------------------------------------------------------------------
+// Products of at most 64 rows: the bytes of b are the cost.  A workgroup takes 16 rows of b (16 gates and
+// their ups) and its waves take turns along k; both operands go from memory straight to the registers of
+// the matrix instruction, and the waves' sums meet in LDS.
+// ---------------------------------------------------------------------------------------------------
+template <class T, bool ALIGNED>
+__device__ __forceinline__ u32x4 row_chunk(const char* row, bool in, int64_t k, int64_t K) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (!in || k >= K) return v;
+    if (ALIGNED) return *reinterpret_cast<const u32x4*>(row + k * (16 / T::chunk));
+    if (T::chunk == 8) {
+        const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + k;
+        for (int e = 0; e < 8; e++)
+            if (k + e < K) v[e >> 1] |= (uint32_t)p[e] << ((e & 1) * 16);
+    } else {
+        const uint8_t* p = reinterpret_cast<const uint8_t*>(row) + k;
+        for (int e = 0; e < 16; e++)
+            if (k + e < K) v[e >> 2] |= (uint32_t)p[e] << ((e & 3) * 8);
+    }
+    return v;
+}
+
+constexpr int kFewWaves = 8;
+
+template <class T, int FI, int EPI, bool ALIGNED>
+__global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(GemmArgs g) {
+    constexpr int NB = EPI == kEpiGated ? 2 : 1;
+    constexpr int BK = 4 * T::chunk;  // k per step of a wave: one chunk per lane
+    __shared__ f32x4 part[kFewWaves][FI * NB][64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int32_t j0 = blockIdx.x * 16, jr = j0 + (lane & 15);
+    const bool jin = jr < g.J;
+    const int ES = 16 / T::chunk;
+    const char* pb[NB];
+    for (int b = 0; b < NB; b++) pb[b] = static_cast<const char*>(g.b) + ((int64_t)b * g.J + (jin ? jr : 0)) * g.ldb * ES;
+    const char* pa[FI];
+    bool ain[FI];
+    for (int i = 0; i < FI; i++) {
+        const int32_t r = i * 16 + (lane & 15);
+        ain[i] = r < g.I;
+        pa[i] = static_cast<const char*>(g.a) + (int64_t)(ain[i] ? r : 0) * g.lda * ES;
+    }
+    f32x4 acc[FI][NB];
+    for (int i = 0; i < FI; i++)
+        for (int b = 0; b < NB; b++) acc[i][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int U = 4;  // steps whose loads are in flight together
+    for (int64_t k0 = (int64_t)wave * BK * U; k0 < g.K; k0 += (int64_t)kFewWaves * BK * U) {
+        u32x4 fb[U][NB], fa[U][FI];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int64_t k = k0 + u * BK + (lane >> 4) * T::chunk;
+#pragma unroll
+            for (int b = 0; b < NB; b++) fb[u][b] = row_chunk<T, ALIGNED>(pb[b], jin, k, g.K);
+#pragma unroll
+            for (int i = 0; i < FI; i++) fa[u][i] = row_chunk<T, ALIGNED>(pa[i], ain[i], k, g.K);
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++)
+#pragma unroll
+            for (int i = 0; i < FI; i++)
+#pragma unroll
+                for (int b = 0; b < NB; b++) acc[i][b] = T::mma(fb[u][b], fa[u][i], acc[i][b]);
+    }
+#pragma unroll
+    for (int i = 0; i < FI; i++)
+#pragma unroll
+        for (int b = 0; b < NB; b++) part[wave][i * NB + b][lane] = acc[i][b];
+    __syncthreads();
+    if (wave >= FI) return;
+    f32x4 v[NB];
+    for (int b = 0; b < NB; b++) {
+        v[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int w = 0; w < kFewWaves; w++) v[b] += part[w][wave * NB + b][lane];
+    }
+    const int32_t i = wave * 16 + (lane & 15), j = j0 + (lane >> 4) * 4;
+    if (i >= g.I || j >= g.J) return;
+    if (EPI == kEpiGated)
+        epi_gated(g.e, v[0], v[NB - 1], i, j, g.J);
+    else
+        epi_linear(g.e, v[0], i, j, g.J);
+}
+
+template <class T, int FI, int EPI>
+hipError_t launch_few_one(bool aligned, const GemmArgs& g, hipStream_t s) {
+    const dim3 grid((unsigned)((g.J + 15) / 16)), block(kFewWaves * 64);
+    if (aligned)
+        hipLaunchKernelGGL((few_rows_kernel<T, FI, EPI, true>), grid, block, 0, s, g);
+    else
+        hipLaunchKernelGGL((few_rows_kernel<T, FI, EPI, false>), grid, block, 0, s, g);
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_few_type(EpiKind kind, bool aligned, const GemmArgs& g, hipStream_t s) {
+    if (kind == kEpiLinear) {
+        if (g.I <= 16) return launch_few_one<T, 1, kEpiLinear>(aligned, g, s);
+        if (g.I <= 32) return launch_few_one<T, 2, kEpiLinear>(aligned, g, s);
+        if (g.I <= 64) return launch_few_one<T, 4, kEpiLinear>(aligned, g, s);
+    } else if (kind == kEpiGated) {
+        if (g.I <= 16) return launch_few_one<T, 1, kEpiGated>(aligned, g, s);
+        if (g.I <= 32) return launch_few_one<T, 2, kEpiGated>(aligned, g, s);
+        if (g.I <= 64) return launch_few_one<T, 4, kEpiGated>(aligned, g, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+}  // namespace gemm
+}  // namespace gsmi

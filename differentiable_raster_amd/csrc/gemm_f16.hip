@@ -1,0 +1,13 @@
+// The matrix products of the neural decoder for operands in f16.
+#include "gemm.h"
+
+namespace gsmi {
+
+hipError_t launch_gemm_f16(TileShape shape, Layout la, Layout lb, EpiKind kind, const GemmArgs& g, hipStream_t s) {
+    return gemm::launch_type<gemm::TF16>(shape, la, lb, kind, g, s);
+}
+hipError_t launch_few_rows_f16(EpiKind kind, bool aligned, const GemmArgs& g, hipStream_t s) {
+    return gemm::launch_few_type<gemm::TF16>(kind, aligned, g, s);
+}
+
+}  // namespace gsmi

@@ -1,0 +1,95 @@
+// Internal declarations of the neural parameter decoder's operators (norm, linear map, gated unit):
+// the argument structs that the host code in neural_api.cpp fills and the launchers it calls.
+#pragma once
+
+#include "common.h"
+
+namespace gsmi {
+
+enum Layout { kRowK = 0, kRowFree = 1 };  // which axis of an operand is contiguous: the summed one, or the free one
+enum EpiKind { kEpiLinear = 0, kEpiGated = 1, kEpiDz = 2, kEpiDGated = 3 };
+
+// What a product's epilogue does with acc[i][j] = sum_k a[i][k] b[j][k], in float32 until the store.
+struct Epi {
+    void* y;               // stored values, at y[i * y_si + j * y_sj]
+    int64_t y_si, y_sj;
+    int32_t y_type;        // gs_type of y, res
+    int32_t y_pad;         // columns j in [J, y_pad) are stored as zeros (y is an operand of a later product)
+    const void* res;       // added after the activation (may be null, may be y)
+    int64_t r_si, r_sj;
+    const float* bias;     // added before the activation (may be null)
+    int32_t bias_on_i;
+    int32_t act;
+    const float* scale_i;  // scales of an 8-bit product (null otherwise)
+    const float* scale_j;
+    const void* dy;        // kEpiDz / kEpiDGated: the gradient of the result, at dy[i * d_si + j * d_sj]
+    int64_t d_si, d_sj;
+    int32_t dy_type;
+    float* colsum;         // kEpiDz / kEpiDGated: per i-strip sums of the stored values over i, [strips][columns]
+};
+
+struct GemmArgs {
+    const void *a, *b;
+    int64_t lda, ldb;      // row strides in elements
+    int32_t I, J;          // result extents; the gated kinds read 2 J rows of b (gates, then ups)
+    int64_t K;             // summed extent
+    int32_t a_cols, b_cols;// kRowFree operands: stored columns (a multiple of a chunk, at least I or J)
+    int32_t splits;        // parts of the summed axis; > 1: raw sums go to partial[splits][I][J]
+    int32_t kt_per_split;  // steps of the summed axis per part
+    float* partial;
+    Epi e;
+};
+
+// Tile shapes of the tiled product.
+enum TileShape { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile64x256 = 3, kTile256x64 = 4, kTileShapes = 5 };
+struct TileDims {
+    int bi, bj, wi;  // rows, columns (of b) and i-strips (waves along i) of a tile
+};
+constexpr TileDims kTileDims[kTileShapes] = {{256, 256, 2}, {128, 128, 2}, {64, 64, 2}, {64, 256, 1}, {256, 64, 4}};
+constexpr int kStepBytes = 128;  // bytes of one row that a step of the summed axis takes
+
+// type: gs_type of both operands (BF16, F16, E4M3).  E4M3: only a, b with kRowK and the forward kinds.
+hipError_t launch_gemm(int type, TileShape shape, Layout la, Layout lb, EpiKind kind, const GemmArgs& g, hipStream_t s);
+hipError_t launch_gemm_bf16(TileShape shape, Layout la, Layout lb, EpiKind kind, const GemmArgs& g, hipStream_t s);
+hipError_t launch_gemm_f16(TileShape shape, Layout la, Layout lb, EpiKind kind, const GemmArgs& g, hipStream_t s);
+hipError_t launch_gemm_e4m3(TileShape shape, Layout la, Layout lb, EpiKind kind, const GemmArgs& g, hipStream_t s);
+hipError_t launch_gemm_reduce(const GemmArgs& g, hipStream_t s);
+
+// Products with at most kFewRows rows of a: every row of b is read once, no tile of a.
+constexpr int kFewRows = 64;
+hipError_t launch_few_rows(int type, EpiKind kind, bool aligned, const GemmArgs& g, hipStream_t s);
+hipError_t launch_few_rows_bf16(EpiKind kind, bool aligned, const GemmArgs& g, hipStream_t s);
+hipError_t launch_few_rows_f16(EpiKind kind, bool aligned, const GemmArgs& g, hipStream_t s);
+hipError_t launch_few_rows_e4m3(EpiKind kind, bool aligned, const GemmArgs& g, hipStream_t s);
+
+// dst[r][c] = src[r * s_row + c * s_col] for c < cols, 0 for c in [cols, ld_dst): an operand in the layout the
+// tiled product reads.  src_type / dst_type: gs_type.
+hipError_t launch_pack(const void* src, int src_type, int64_t s_row, int64_t s_col, int64_t rows, int32_t cols,
+                       void* dst, int dst_type, int64_t ld_dst, hipStream_t s);
+// out[c] = sum_r in[r * s_row + c * s_col], in a fixed order.  partial: colsum_partial_floats(rows, cols) floats.
+size_t colsum_partial_floats(int64_t rows, int32_t cols);
+hipError_t launch_colsum(const void* in, int type, int64_t s_row, int64_t s_col, int64_t rows, int32_t cols,
+                         float* partial, float* out, hipStream_t s);
+
+struct NormArgs {
+    int64_t rows;
+    int32_t width;
+    float eps;
+    int32_t normalize;  // 0: quantize the rows as they are
+    const void *x, *r;
+    void *s, *y;
+    uint8_t* q;
+    float* q_scale;
+    const float* w;
+    int64_t ld_x, ld_r, ld_s, ld_y;
+    // backward
+    const void *dy, *ds;
+    void* dx;
+    float* partial;  // [norm_groups(rows, width)][width]
+};
+hipError_t launch_norm_fwd(int type, const NormArgs& a, hipStream_t s);
+hipError_t launch_norm_bwd(int type, const NormArgs& a, int32_t groups, hipStream_t s);
+int32_t norm_groups(int64_t rows, int32_t width);
+constexpr int kNormMaxWidth = 32768;
+
+}  // namespace gsmi

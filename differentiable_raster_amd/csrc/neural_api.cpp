@@ -1,0 +1,473 @@
+// Host side of the neural decoder's entry points: argument validation, the choice of kernel, tile and
+// split by sizes and types, workspace carving and launches.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "neural.h"
+
+using namespace gsmi;
+
+namespace {
+
+#define BAD(...) return api_fail(GS_ERR_INVALID_ARGUMENT, __VA_ARGS__)
+
+gs_status launched(hipError_t e, const char* what) {
+    if (e == hipSuccess) return GS_OK;
+    return api_fail(GS_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+}
+
+size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
+int64_t round8(int64_t n) { return (n + 7) & ~int64_t(7); }
+int elem_bytes(int type) { return type == GS_TYPE_F32 ? 4 : type == GS_TYPE_E4M3 ? 1 : 2; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool aligned_to(const void* p, int type) { return reinterpret_cast<uintptr_t>(p) % elem_bytes(type) == 0; }
+
+struct Carver {
+    char* base;
+    size_t used = 0;
+    void* take(size_t bytes) {
+        void* p = base ? base + used : nullptr;
+        used += align256(bytes);
+        return p;
+    }
+};
+
+// ---------------------------------------------------------------------------------------------------
+// Tile shape and split of a tiled product.
+// ---------------------------------------------------------------------------------------------------
+struct Tiling {
+    TileShape shape;
+    int32_t splits, kt_per_split;
+    size_t partial_bytes(int64_t I, int64_t J) const { return splits > 1 ? (size_t)splits * I * J * 4 : 0; }
+};
+
+int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+Tiling choose(int type, int64_t I, int64_t J, int64_t K, bool paired, bool may_split) {
+    const int64_t bk = kStepBytes / elem_bytes(type), kt = div_up(K, bk) > 0 ? div_up(K, bk) : 1;
+    const int64_t cols = paired ? 2 * J : J;
+    // steps that a CU takes per microsecond of a 256 x 256 tile's step, by shape
+    static const double eff[kTileShapes] = {1.0, 0.8, 0.5, 0.65, 0.65};
+    Tiling best{kTile64, 1, (int32_t)kt};
+    double best_t = 1e300;
+    for (int s = 0; s < kTileShapes; s++) {
+        const TileDims d = kTileDims[s];
+        const int64_t tiles = div_up(I, d.bi) * div_up(cols, d.bj);
+        const double step = 0.7 * (double)(d.bi * d.bj) / 65536.0 / eff[s];  // us per step
+        for (int64_t splits = 1; splits <= (may_split ? 64 : 1); splits *= 2) {
+            if (splits > 1 && kt / splits < 4) break;
+            const int64_t per = div_up(kt, splits);
+            double t = (double)div_up(tiles * splits, 256) * ((double)per * step + 2.0);
+            if (splits > 1) t += 3.0 + (double)splits * I * J * 8.0 / 3e6;  // the raw sums, written and read
+            if (t < best_t * 0.999) {
+                best_t = t;
+                best = Tiling{(TileShape)s, (int32_t)div_up(kt, per), (int32_t)per};
+            }
+        }
+    }
+    return best;
+}
+
+void set_tiling(GemmArgs& g, const Tiling& t, void* partial) {
+    g.splits = t.splits;
+    g.kt_per_split = t.kt_per_split;
+    g.partial = t.splits > 1 ? static_cast<float*>(partial) : nullptr;
+}
+
+hipError_t tiled(int type, const Tiling& t, Layout la, Layout lb, EpiKind kind, const GemmArgs& g, hipStream_t s) {
+    hipError_t e = launch_gemm(type, t.shape, la, lb, kind, g, s);
+    if (e == hipSuccess && g.partial) e = launch_gemm_reduce(g, s);
+    return e;
+}
+
+// ---------------------------------------------------------------------------------------------------
+// Linear map and gated unit
+// ---------------------------------------------------------------------------------------------------
+struct Dims {
+    int64_t m, k, n;  // rows, summed width, rows of the weight
+    int64_t ld_x, ld_w, ld_y, ld_r;
+    int32_t chunk;    // elements of 16 bytes
+    bool pack_x, pack_w;
+};
+
+gs_status check_desc(const gs_linear_desc* d, bool gated, bool backward, Dims* o) {
+    if (!d) BAD("descriptor is null");
+    if (d->rows < 0) BAD("rows=%d", d->rows);
+    if (d->in < 1 || d->in > GS_LINEAR_MAX_WIDTH) BAD("in=%d outside 1..%d", d->in, GS_LINEAR_MAX_WIDTH);
+    if (d->out < 1 || d->out > GS_LINEAR_MAX_WIDTH) BAD("out=%d outside 1..%d", d->out, GS_LINEAR_MAX_WIDTH);
+    if (d->type != GS_TYPE_BF16 && d->type != GS_TYPE_F16 && d->type != GS_TYPE_E4M3) BAD("type=%d", d->type);
+    if (backward && d->type == GS_TYPE_E4M3) return api_fail(GS_ERR_UNSUPPORTED, "8-bit operands have no backward");
+    if (d->y_type != GS_TYPE_BF16 && d->y_type != GS_TYPE_F16 && d->y_type != GS_TYPE_F32) BAD("y_type=%d", d->y_type);
+    if (backward && d->grad_type != GS_TYPE_F32 && d->grad_type != d->type) BAD("grad_type=%d", d->grad_type);
+    if (d->act < GS_ACT_NONE || d->act > GS_ACT_GELU) BAD("act=%d", d->act);
+    if (d->y_channel_major != 0 && (d->y_channel_major != 1 || gated)) BAD("y_channel_major=%d", d->y_channel_major);
+    o->m = d->rows;
+    o->k = d->in;
+    o->n = gated ? 2 * (int64_t)d->out : d->out;
+    const int64_t y_width = d->y_channel_major ? d->rows : d->out, r_width = backward ? d->in : y_width;
+    o->ld_x = d->ld_x ? d->ld_x : d->in;
+    o->ld_w = d->ld_w ? d->ld_w : d->in;
+    o->ld_y = d->ld_y ? d->ld_y : y_width;
+    o->ld_r = d->ld_r ? d->ld_r : r_width;
+    if (o->ld_x < d->in || o->ld_x >= (1 << 21)) BAD("ld_x=%lld for in=%d", (long long)d->ld_x, d->in);
+    if (o->ld_w < d->in || o->ld_w >= (1 << 21)) BAD("ld_w=%lld for in=%d", (long long)d->ld_w, d->in);
+    if (o->ld_y < y_width || o->ld_y >= (int64_t(1) << 40)) BAD("ld_y=%lld for a row of %lld", (long long)d->ld_y, (long long)y_width);
+    if (o->ld_r < r_width || o->ld_r >= (int64_t(1) << 40)) BAD("ld_r=%lld for a row of %lld", (long long)d->ld_r, (long long)r_width);
+    o->chunk = 16 / elem_bytes(d->type);
+    o->pack_x = d->in % o->chunk != 0 || o->ld_x % o->chunk != 0;
+    o->pack_w = d->in % o->chunk != 0 || o->ld_w % o->chunk != 0;
+    const int64_t ld_w_used = o->pack_w ? div_up(d->in, o->chunk) * o->chunk : o->ld_w;
+    if (gated && o->n * (ld_w_used > o->ld_w ? ld_w_used : o->ld_w) >= (int64_t(1) << 29))
+        return api_fail(GS_ERR_UNSUPPORTED, "gated weights of %lld x %lld elements", (long long)o->n, (long long)o->ld_w);
+    return GS_OK;
+}
+
+bool use_few_rows(const Dims& o) { return o.m <= kFewRows; }
+
+Tiling forward_tiling(const gs_linear_desc* d, const Dims& o, bool gated) {
+    if (gated) return choose(d->type, o.m, d->out, o.k, true, false);
+    if (d->y_channel_major) return choose(d->type, o.n, o.m, o.k, false, true);
+    return choose(d->type, o.m, o.n, o.k, false, true);
+}
+
+struct ForwardWs {
+    void *x, *w, *partial;
+};
+ForwardWs carve_forward(void* ws, const gs_linear_desc* d, const Dims& o, bool gated, size_t* bytes) {
+    Carver c{static_cast<char*>(ws)};
+    ForwardWs f{nullptr, nullptr, nullptr};
+    if (o.m > 0 && !use_few_rows(o)) {
+        const size_t kp = (size_t)div_up(o.k, o.chunk) * 16;
+        if (o.pack_x) f.x = c.take((size_t)o.m * kp);
+        if (o.pack_w) f.w = c.take((size_t)o.n * kp);
+        const size_t p = forward_tiling(d, o, gated).partial_bytes(o.m, o.n);
+        if (p) f.partial = c.take(p);
+    }
+    *bytes = c.used;
+    return f;
+}
+
+gs_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
+    if (need == 0) return GS_OK;
+    if (!ws) BAD("workspace is null (%zu bytes needed)", need);
+    if (ws_bytes < need) BAD("workspace of %zu bytes, %zu needed", ws_bytes, need);
+    if ((reinterpret_cast<uintptr_t>(ws) & 255) != 0) BAD("workspace is not 256-byte aligned");
+    return GS_OK;
+}
+
+gs_status forward(const gs_linear_desc* d, bool gated, const void* x, const float* x_scale, const void* weight,
+                  const float* w_scale, const float* bias, const void* residual, void* y, void* ws, size_t ws_bytes,
+                  void* stream) {
+    api_clear();
+    Dims o;
+    gs_status st = check_desc(d, gated, false, &o);
+    if (st != GS_OK) return st;
+    const bool scaled = d->type == GS_TYPE_E4M3;
+    if (o.m == 0) return GS_OK;
+    if (!x || !weight || !y) BAD("x, weight or the result is null");
+    if (scaled != (x_scale != nullptr) || scaled != (w_scale != nullptr)) BAD("scales go with 8-bit operands, both of them");
+    if (!aligned16(x) || !aligned16(weight)) BAD("x and weight must be 16-byte aligned");
+    if (!aligned_to(y, d->y_type) || !aligned_to(residual, d->y_type) || !aligned_to(bias, GS_TYPE_F32) ||
+        !aligned_to(x_scale, GS_TYPE_F32) || !aligned_to(w_scale, GS_TYPE_F32))
+        BAD("an array is not aligned to its element");
+    size_t need = 0;
+    carve_forward(nullptr, d, o, gated, &need);
+    st = check_ws(ws, ws_bytes, need);
+    if (st != GS_OK) return st;
+    const ForwardWs f = carve_forward(ws, d, o, gated, &need);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+
+    GemmArgs g;
+    std::memset(&g, 0, sizeof(g));
+    g.K = o.k;
+    g.splits = 1;
+    g.e.y = y;
+    g.e.y_type = d->y_type;
+    g.e.res = residual;
+    g.e.bias = bias;
+    g.e.act = d->act;
+    const EpiKind kind = gated ? kEpiGated : kEpiLinear;
+    const bool cm = d->y_channel_major != 0;
+
+    if (use_few_rows(o)) {
+        g.a = x, g.lda = o.ld_x, g.b = weight, g.ldb = o.ld_w;
+        g.I = d->rows, g.J = d->out;
+        g.e.y_si = cm ? 1 : o.ld_y, g.e.y_sj = cm ? o.ld_y : 1;
+        g.e.r_si = cm ? 1 : o.ld_r, g.e.r_sj = cm ? o.ld_r : 1;
+        g.e.scale_i = x_scale, g.e.scale_j = w_scale;
+        return launched(launch_few_rows(d->type, kind, !o.pack_x && !o.pack_w, g, s), "product of few rows");
+    }
+    const int64_t kp = div_up(o.k, o.chunk) * o.chunk;
+    hipError_t e = hipSuccess;
+    if (o.pack_x) {
+        e = launch_pack(x, d->type, o.ld_x, 1, o.m, d->in, f.x, d->type, kp, s);
+        x = f.x, o.ld_x = kp;
+    }
+    if (e == hipSuccess && o.pack_w) {
+        e = launch_pack(weight, d->type, o.ld_w, 1, o.n, d->in, f.w, d->type, kp, s);
+        weight = f.w, o.ld_w = kp;
+    }
+    if (e != hipSuccess) return launched(e, "operand copy");
+    if (cm) {  // the result's rows are channels: weight is the first operand
+        g.a = weight, g.lda = o.ld_w, g.b = x, g.ldb = o.ld_x;
+        g.I = d->out, g.J = d->rows;
+        g.e.scale_i = w_scale, g.e.scale_j = x_scale;
+        g.e.bias_on_i = 1;
+    } else {
+        g.a = x, g.lda = o.ld_x, g.b = weight, g.ldb = o.ld_w;
+        g.I = d->rows, g.J = d->out;
+        g.e.scale_i = x_scale, g.e.scale_j = w_scale;
+    }
+    g.e.y_si = o.ld_y, g.e.y_sj = 1;
+    g.e.r_si = o.ld_r, g.e.r_sj = 1;
+    const Tiling t = forward_tiling(d, o, gated);
+    set_tiling(g, t, f.partial);
+    return launched(tiled(d->type, t, kRowK, kRowK, kind, g, s), "matrix product");
+}
+
+// The backward's buffers and tilings, all from the descriptor.
+struct BackwardPlan {
+    bool need_dz;      // dz is no array that the caller has: an own one, [rows][np]
+    bool need_z;       // dz needs the pre-activation
+    int64_t kp, np;    // padded widths of x / weight copies and of dz
+    Tiling tz, tx, tw;
+    int64_t strips;    // rows of the column sums' partials out of the z product
+    void *x, *w, *dz, *sums, *sums2, *partial;
+    size_t bytes;
+};
+
+BackwardPlan plan_backward(const gs_linear_desc* d, const Dims& o, bool gated, void* ws) {
+    BackwardPlan p;
+    std::memset(&p, 0, sizeof(p));
+    Carver c{static_cast<char*>(ws)};
+    const int es = elem_bytes(d->type);
+    p.need_z = gated || d->act != GS_ACT_NONE;
+    p.need_dz = p.need_z || d->y_type != d->type || d->y_channel_major || o.n % 8 != 0 || o.ld_y % 8 != 0 || o.ld_y >= (1 << 21);
+    p.kp = round8(o.k);
+    p.np = round8(o.n);
+    p.tz = choose(d->type, o.m > 0 ? o.m : 1, d->out, o.k, gated, false);
+    p.tx = choose(d->type, o.m > 0 ? o.m : 1, o.k, o.n, false, true);
+    p.tw = choose(d->type, o.n, o.k, o.m, false, true);
+    const TileDims td = kTileDims[p.tz.shape];
+    p.strips = div_up(o.m > 0 ? o.m : 1, td.bi) * td.wi;
+    if (o.pack_x) p.x = c.take((size_t)o.m * p.kp * es);
+    if (o.pack_w) p.w = c.take((size_t)o.n * p.kp * es);
+    if (p.need_dz) p.dz = c.take((size_t)o.m * p.np * es);
+    if (p.need_z) p.sums = c.take((size_t)p.strips * o.n * 4);
+    p.sums2 = c.take(colsum_partial_floats(p.need_z ? p.strips : o.m, (int32_t)o.n) * 4);
+    const size_t px = p.tx.partial_bytes(o.m, o.k), pw = p.tw.partial_bytes(o.n, o.k);
+    p.partial = c.take(px > pw ? px : pw);
+    p.bytes = c.used;
+    return p;
+}
+
+gs_status backward(const gs_linear_desc* d, bool gated, const void* x, const void* weight, const float* bias, const void* dy,
+                   void* dx, void* dweight, float* dbias, void* ws, size_t ws_bytes, void* stream) {
+    api_clear();
+    Dims o;
+    gs_status st = check_desc(d, gated, true, &o);
+    if (st != GS_OK) return st;
+    if (o.m > 0 && (!x || !weight || !dy)) BAD("x, weight or the result's gradient is null");
+    if (!aligned16(x) || !aligned16(weight) || !aligned16(dy)) BAD("x, weight and the result's gradient must be 16-byte aligned");
+    if (!aligned_to(bias, GS_TYPE_F32) || !aligned_to(dx, d->type) || !aligned_to(dweight, d->grad_type) || !aligned_to(dbias, GS_TYPE_F32))
+        BAD("a gradient is not aligned to its element");
+    st = check_ws(ws, ws_bytes, plan_backward(d, o, gated, nullptr).bytes);
+    if (st != GS_OK) return st;
+    const BackwardPlan p = plan_backward(d, o, gated, ws);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const bool cm = d->y_channel_major != 0;
+    hipError_t e = hipSuccess;
+
+    if (o.m > 0 && o.pack_x && (p.need_z || dweight)) {
+        e = launch_pack(x, d->type, o.ld_x, 1, o.m, d->in, p.x, d->type, p.kp, s);
+        if (e != hipSuccess) return launched(e, "operand copy");
+    }
+    if (o.m > 0 && o.pack_w && (p.need_z || dx)) {
+        e = launch_pack(weight, d->type, o.ld_w, 1, o.n, d->in, p.w, d->type, p.kp, s);
+        if (e != hipSuccess) return launched(e, "operand copy");
+    }
+    const void* xo = o.pack_x ? p.x : x;
+    const void* wo = o.pack_w ? p.w : weight;
+    const int64_t ldx = o.pack_x ? p.kp : o.ld_x, ldw = o.pack_w ? p.kp : o.ld_w;
+    const int64_t d_si = cm ? 1 : o.ld_y, d_sj = cm ? o.ld_y : 1;
+
+    // dz, and the column sums of its unrounded values
+    if (o.m > 0 && p.need_z) {
+        GemmArgs g;
+        std::memset(&g, 0, sizeof(g));
+        g.a = xo, g.lda = ldx, g.b = wo, g.ldb = ldw;
+        g.I = d->rows, g.J = d->out, g.K = o.k;
+        g.e.y = p.dz, g.e.y_si = p.np, g.e.y_sj = 1, g.e.y_type = d->type, g.e.y_pad = (int32_t)p.np;
+        g.e.bias = bias, g.e.act = d->act;
+        g.e.dy = dy, g.e.dy_type = d->y_type, g.e.d_si = d_si, g.e.d_sj = d_sj;
+        g.e.colsum = dbias ? static_cast<float*>(p.sums) : nullptr;
+        set_tiling(g, p.tz, nullptr);
+        e = tiled(d->type, p.tz, kRowK, kRowK, gated ? kEpiDGated : kEpiDz, g, s);
+        if (e != hipSuccess) return launched(e, "projection of the backward");
+    } else if (o.m > 0 && p.need_dz && (dx || dweight)) {
+        e = launch_pack(dy, d->y_type, d_si, d_sj, o.m, (int32_t)o.n, p.dz, d->type, p.np, s);
+        if (e != hipSuccess) return launched(e, "gradient copy");
+    }
+    if (dbias) {
+        if (p.need_z)
+            e = launch_colsum(p.sums, GS_TYPE_F32, o.n, 1, o.m > 0 ? p.strips : 0, (int32_t)o.n, static_cast<float*>(p.sums2), dbias, s);
+        else
+            e = launch_colsum(dy, d->y_type, d_si, d_sj, o.m, (int32_t)o.n, static_cast<float*>(p.sums2), dbias, s);
+        if (e != hipSuccess) return launched(e, "bias gradient");
+    }
+    const void* dz = p.need_dz ? p.dz : dy;
+    const int64_t ldz = p.need_dz ? p.np : o.ld_y;
+    if (dx && o.m > 0) {
+        GemmArgs g;
+        std::memset(&g, 0, sizeof(g));
+        g.a = dz, g.lda = ldz, g.b = wo, g.ldb = ldw;
+        g.I = d->rows, g.J = d->in, g.K = o.n, g.b_cols = (int32_t)p.kp;
+        g.e.y = dx, g.e.y_si = o.ld_r, g.e.y_sj = 1, g.e.y_type = d->type;
+        set_tiling(g, p.tx, p.partial);
+        e = tiled(d->type, p.tx, kRowK, kRowFree, kEpiLinear, g, s);
+        if (e != hipSuccess) return launched(e, "input gradient");
+    }
+    if (dweight) {
+        GemmArgs g;
+        std::memset(&g, 0, sizeof(g));
+        g.a = dz, g.lda = ldz, g.b = xo, g.ldb = ldx;
+        g.I = (int32_t)o.n, g.J = d->in, g.K = o.m, g.a_cols = (int32_t)p.np, g.b_cols = (int32_t)p.kp;
+        g.e.y = dweight, g.e.y_si = o.k, g.e.y_sj = 1, g.e.y_type = d->grad_type;
+        set_tiling(g, p.tw, p.partial);
+        e = tiled(d->type, p.tw, kRowFree, kRowFree, kEpiLinear, g, s);
+        if (e != hipSuccess) return launched(e, "weight gradient");
+    }
+    return GS_OK;
+}
+
+size_t forward_ws(const gs_linear_desc* d, bool gated) {
+    Dims o;
+    if (check_desc(d, gated, false, &o) != GS_OK) return 0;
+    size_t bytes = 0;
+    carve_forward(nullptr, d, o, gated, &bytes);
+    return bytes;
+}
+size_t backward_ws(const gs_linear_desc* d, bool gated) {
+    Dims o;
+    if (check_desc(d, gated, true, &o) != GS_OK) return 0;
+    return plan_backward(d, o, gated, nullptr).bytes;
+}
+
+// ---------------------------------------------------------------------------------------------------
+// Norm
+// ---------------------------------------------------------------------------------------------------
+gs_status check_norm(const gs_norm_desc* d, NormArgs* a) {
+    if (!d) BAD("descriptor is null");
+    if (d->rows < 0) BAD("rows=%d", d->rows);
+    if (d->width < 1 || d->width > GS_NORM_MAX_WIDTH) BAD("width=%d outside 1..%d", d->width, GS_NORM_MAX_WIDTH);
+    if (d->type != GS_TYPE_F32 && d->type != GS_TYPE_BF16 && d->type != GS_TYPE_F16) BAD("type=%d", d->type);
+    if (!(d->eps >= 0.0f) || !std::isfinite(d->eps)) BAD("eps outside [0, inf)");
+    const int64_t lds[4] = {d->ld_x, d->ld_r, d->ld_s, d->ld_y};
+    for (int64_t ld : lds)
+        if (ld != 0 && (ld < d->width || ld >= (int64_t(1) << 31))) BAD("row stride %lld for width %d", (long long)ld, d->width);
+    std::memset(a, 0, sizeof(*a));
+    a->rows = d->rows;
+    a->width = d->width;
+    a->eps = d->eps;
+    a->ld_x = d->ld_x ? d->ld_x : d->width;
+    a->ld_r = d->ld_r ? d->ld_r : d->width;
+    a->ld_s = d->ld_s ? d->ld_s : d->width;
+    a->ld_y = d->ld_y ? d->ld_y : d->width;
+    return GS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gs_status gs_rmsnorm(const gs_norm_desc* d, const void* x, const void* residual, const float* weight, void* s, void* y,
+                     void* q, float* q_scale, void* stream) {
+    api_clear();
+    NormArgs a;
+    gs_status st = check_norm(d, &a);
+    if (st != GS_OK) return st;
+    if (d->rows == 0) return GS_OK;
+    if (!s && !y && !q) BAD("no output is given");
+    if ((q != nullptr) != (q_scale != nullptr)) BAD("q and q_scale go together");
+    if (!x) BAD("x is null");
+    if (!aligned_to(x, d->type) || !aligned_to(residual, d->type) || !aligned_to(s, d->type) || !aligned_to(y, d->type) ||
+        !aligned_to(weight, GS_TYPE_F32) || !aligned_to(q_scale, GS_TYPE_F32))
+        BAD("an array is not aligned to its element");
+    a.normalize = 1;
+    a.x = x, a.r = residual, a.w = weight, a.s = s, a.y = y, a.q = static_cast<uint8_t*>(q), a.q_scale = q_scale;
+    return launched(launch_norm_fwd(d->type, a, static_cast<hipStream_t>(stream)), "gs_rmsnorm launch");
+}
+
+gs_status gs_quantize_rows(const gs_norm_desc* d, const void* x, void* q, float* q_scale, void* stream) {
+    api_clear();
+    NormArgs a;
+    gs_status st = check_norm(d, &a);
+    if (st != GS_OK) return st;
+    if (d->rows == 0) return GS_OK;
+    if (!x || !q || !q_scale) BAD("x, q or q_scale is null");
+    if (!aligned_to(x, d->type) || !aligned_to(q_scale, GS_TYPE_F32)) BAD("an array is not aligned to its element");
+    a.x = x, a.q = static_cast<uint8_t*>(q), a.q_scale = q_scale;
+    return launched(launch_norm_fwd(d->type, a, static_cast<hipStream_t>(stream)), "gs_quantize_rows launch");
+}
+
+size_t gs_rmsnorm_bwd_workspace_size(const gs_norm_desc* d) {
+    NormArgs a;
+    if (check_norm(d, &a) != GS_OK) return 0;
+    const int32_t groups = norm_groups(d->rows, d->width);
+    return align256((size_t)groups * d->width * 4) + align256(colsum_partial_floats(groups, d->width) * 4);
+}
+
+gs_status gs_rmsnorm_bwd(const gs_norm_desc* d, const void* s, const float* weight, const void* dy, const void* ds, void* dx,
+                         float* dweight, void* ws, size_t ws_bytes, void* stream) {
+    api_clear();
+    NormArgs a;
+    gs_status st = check_norm(d, &a);
+    if (st != GS_OK) return st;
+    if (d->rows > 0 && (!s || !dy || !dx)) BAD("s, dy or dx is null");
+    if (!aligned_to(s, d->type) || !aligned_to(dy, d->type) || !aligned_to(ds, d->type) || !aligned_to(dx, d->type) ||
+        !aligned_to(weight, GS_TYPE_F32) || !aligned_to(dweight, GS_TYPE_F32))
+        BAD("an array is not aligned to its element");
+    const int32_t groups = norm_groups(d->rows, d->width);
+    Carver c{static_cast<char*>(ws)};
+    float* partial = static_cast<float*>(c.take((size_t)groups * d->width * 4));
+    float* partial2 = static_cast<float*>(c.take(colsum_partial_floats(groups, d->width) * 4));
+    if (dweight) {
+        st = check_ws(ws, ws_bytes, c.used);
+        if (st != GS_OK) return st;
+    }
+    hipStream_t hs = static_cast<hipStream_t>(stream);
+    if (d->rows > 0) {
+        a.s = const_cast<void*>(s), a.w = weight, a.dy = dy, a.ds = ds, a.dx = dx;
+        a.partial = dweight ? partial : nullptr;
+        st = launched(launch_norm_bwd(d->type, a, groups, hs), "gs_rmsnorm_bwd launch");
+        if (st != GS_OK) return st;
+    }
+    if (!dweight) return GS_OK;
+    return launched(launch_colsum(partial, GS_TYPE_F32, d->width, 1, groups, d->width, partial2, dweight, hs), "weight gradient");
+}
+
+size_t gs_linear_workspace_size(const gs_linear_desc* d) { return forward_ws(d, false); }
+gs_status gs_linear(const gs_linear_desc* d, const void* x, const float* x_scale, const void* weight, const float* w_scale,
+                    const float* bias, const void* residual, void* y, void* ws, size_t ws_bytes, void* stream) {
+    return forward(d, false, x, x_scale, weight, w_scale, bias, residual, y, ws, ws_bytes, stream);
+}
+size_t gs_linear_bwd_workspace_size(const gs_linear_desc* d) { return backward_ws(d, false); }
+gs_status gs_linear_bwd(const gs_linear_desc* d, const void* x, const void* weight, const float* bias, const void* dy,
+                        void* dx, void* dweight, float* dbias, void* ws, size_t ws_bytes, void* stream) {
+    return backward(d, false, x, weight, bias, dy, dx, dweight, dbias, ws, ws_bytes, stream);
+}
+
+size_t gs_gated_workspace_size(const gs_linear_desc* d) { return forward_ws(d, true); }
+gs_status gs_gated(const gs_linear_desc* d, const void* x, const float* x_scale, const void* weight, const float* w_scale,
+                   const float* bias, void* h, void* ws, size_t ws_bytes, void* stream) {
+    return forward(d, true, x, x_scale, weight, w_scale, bias, nullptr, h, ws, ws_bytes, stream);
+}
+size_t gs_gated_bwd_workspace_size(const gs_linear_desc* d) { return backward_ws(d, true); }
+gs_status gs_gated_bwd(const gs_linear_desc* d, const void* x, const void* weight, const float* bias, const void* dh, void* dx,
+                       void* dweight, float* dbias, void* ws, size_t ws_bytes, void* stream) {
+    return backward(d, true, x, weight, bias, dh, dx, dweight, dbias, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

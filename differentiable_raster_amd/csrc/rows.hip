@@ -1,0 +1,462 @@
+// Row kernels of the neural decoder: the root-mean-square norm with the residual's addition and its
+// backward, 8-bit rows with scales, operand copies, column sums and the join of a split product.  All are
+// bound by memory: each value is read once and written once, whole rows stay in registers between the
+// statistics and the result, and every sum over rows has a fixed order.
+#include "elem.h"
+#include "neural.h"
+
+namespace gsmi {
+namespace {
+
+constexpr float kE4m3Max = 448.0f;
+
+// Eight neighbours c..c+7 of a row of `width` values at p, as float32; zeros past the end.
+template <class T>
+__device__ __forceinline__ void load8(const void* base, int64_t at, int32_t c, int32_t width, bool vec, float (&v)[8]);
+template <class T>
+__device__ __forceinline__ void store8(void* base, int64_t at, int32_t c, int32_t width, bool vec, const float (&v)[8]);
+
+struct F32 {
+    static constexpr int type = GS_TYPE_F32;
+};
+struct Bf16 {
+    static constexpr int type = GS_TYPE_BF16;
+};
+struct F16 {
+    static constexpr int type = GS_TYPE_F16;
+};
+
+template <class T>
+__device__ __forceinline__ void load8(const void* base, int64_t at, int32_t c, int32_t width, bool vec, float (&v)[8]) {
+    if (vec) {
+        if (c >= width) {
+            for (int k = 0; k < 8; k++) v[k] = 0.0f;
+        } else if (T::type == GS_TYPE_F32) {
+            const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + at + c);
+            const f32x4 a = p[0], b = p[1];
+            for (int k = 0; k < 4; k++) {
+                v[k] = a[k];
+                v[4 + k] = b[k];
+            }
+        } else {
+            const u32x4 p = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + at + c);
+            for (int k = 0; k < 8; k++) {
+                const uint16_t h = (uint16_t)(p[k >> 1] >> ((k & 1) * 16));
+                v[k] = T::type == GS_TYPE_BF16 ? bf16_to_f32(h) : f16_to_f32(h);
+            }
+        }
+    } else {
+        for (int k = 0; k < 8; k++) v[k] = c + k < width ? load_elem(base, T::type, at + c + k) : 0.0f;
+    }
+}
+
+template <class T>
+__device__ __forceinline__ void store8(void* base, int64_t at, int32_t c, int32_t width, bool vec, const float (&v)[8]) {
+    if (vec) {
+        if (c >= width) return;
+        if (T::type == GS_TYPE_F32) {
+            f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(base) + at + c);
+            p[0] = f32x4{v[0], v[1], v[2], v[3]};
+            p[1] = f32x4{v[4], v[5], v[6], v[7]};
+        } else {
+            u32x4 p;
+            for (int k = 0; k < 4; k++) p[k] = pack2(v[2 * k], v[2 * k + 1], T::type);
+            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(base) + at + c) = p;
+        }
+    } else {
+        for (int k = 0; k < 8; k++)
+            if (c + k < width) store_elem(base, T::type, at + c + k, v[k]);
+    }
+}
+
+__device__ __forceinline__ bool vec8(const void* p, int64_t ld, int32_t width, int type) {
+    const int mask = type == GS_TYPE_F32 ? 3 : 7;
+    return (width & 7) == 0 && (ld & mask) == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
+}
+
+// Sum (or maximum of bit patterns) over the NT threads that share a row.
+template <int NT>
+__device__ __forceinline__ float row_sum(float v, float* lds) {
+#pragma unroll
+    for (int m = 1; m < (NT < 64 ? NT : 64); m <<= 1) v += __shfl_xor(v, m);
+    if (NT > 64) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.0f;
+        for (int w = 0; w < NT / 64; w++) v += lds[w];
+    }
+    return v;
+}
+template <int NT>
+__device__ __forceinline__ uint32_t row_umax(uint32_t v, float* lds) {
+#pragma unroll
+    for (int m = 1; m < (NT < 64 ? NT : 64); m <<= 1) {
+        const uint32_t o = __shfl_xor(v, m);
+        v = o > v ? o : v;
+    }
+    if (NT > 64) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = __uint_as_float(v);
+        __syncthreads();
+        v = 0;
+        for (int w = 0; w < NT / 64; w++) {
+            const uint32_t o = __float_as_uint(lds[w]);
+            v = o > v ? o : v;
+        }
+    }
+    return v;
+}
+
+__device__ __forceinline__ float to_range(float v) {  // NaN stays NaN
+    return v > kE4m3Max ? kE4m3Max : (v < -kE4m3Max ? -kE4m3Max : v);
+}
+
+constexpr int rows_per_block(int nt) { return nt < 256 ? 256 / nt : 1; }
+constexpr int block_of(int nt) { return nt < 256 ? 256 : nt; }
+
+// NT threads per row, NC chunks of 8 values per thread.
+template <class T, int NT, int NC>
+__global__ __launch_bounds__(block_of(NT)) void norm_fwd_kernel(NormArgs a) {
+    __shared__ float lds[16];
+    const int64_t row = (int64_t)blockIdx.x * rows_per_block(NT) + threadIdx.x / NT;
+    const int t = threadIdx.x % NT;
+    if (NT <= 64 && row >= a.rows) return;  // NT > 64: one row per block, all of them in range
+    const bool vx = vec8(a.x, a.ld_x, a.width, T::type);
+    float v[NC][8];
+    float sq = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NC; c++) load8<T>(a.x, row * a.ld_x, (c * NT + t) * 8, a.width, vx, v[c]);
+    if (a.r) {
+        const bool vr = vec8(a.r, a.ld_r, a.width, T::type);
+#pragma unroll
+        for (int c = 0; c < NC; c++) {
+            float r[8];
+            load8<T>(a.r, row * a.ld_r, (c * NT + t) * 8, a.width, vr, r);
+            for (int k = 0; k < 8; k++) v[c][k] += r[k];
+        }
+    }
+    if (a.s) {
+        const bool vs = vec8(a.s, a.ld_s, a.width, T::type);
+#pragma unroll
+        for (int c = 0; c < NC; c++) store8<T>(a.s, row * a.ld_s, (c * NT + t) * 8, a.width, vs, v[c]);
+    }
+    if (a.normalize) {
+        if (!a.y && !a.q) return;
+#pragma unroll
+        for (int c = 0; c < NC; c++)
+            for (int k = 0; k < 8; k++) sq = fmaf(v[c][k], v[c][k], sq);
+        const float ms = row_sum<NT>(sq, lds) / (float)a.width;
+        const float rstd = 1.0f / sqrtf(ms + a.eps);
+#pragma unroll
+        for (int c = 0; c < NC; c++) {
+            float w[8];
+            if (a.w) load8<F32>(a.w, 0, (c * NT + t) * 8, a.width, vec8(a.w, 8, a.width, GS_TYPE_F32), w);
+            for (int k = 0; k < 8; k++) v[c][k] = v[c][k] * rstd * (a.w ? w[k] : 1.0f);
+        }
+    }
+    if (a.y) {
+        const bool vy = vec8(a.y, a.ld_y, a.width, T::type);
+#pragma unroll
+        for (int c = 0; c < NC; c++) store8<T>(a.y, row * a.ld_y, (c * NT + t) * 8, a.width, vy, v[c]);
+    }
+    if (a.q) {
+        // the largest magnitude by its bit pattern: a NaN's is larger than every number's
+        uint32_t most = 0;
+#pragma unroll
+        for (int c = 0; c < NC; c++)
+            for (int k = 0; k < 8; k++) {
+                const uint32_t b = (c * NT + t) * 8 + k < a.width ? __float_as_uint(v[c][k]) & 0x7FFFFFFFu : 0u;
+                most = b > most ? b : most;
+            }
+        const float amax = __uint_as_float(row_umax<NT>(most, lds));
+        // rows below 1e-30 count as zeros: 448 / amax would leave the float32 range
+        const bool zero = amax < 1e-30f;
+        if (t == 0) a.q_scale[row] = zero ? 0.0f : amax / kE4m3Max;
+        const float inv = zero ? 0.0f : kE4m3Max / amax;
+        const bool vq = (a.width & 7) == 0 && (a.ld_y & 7) == 0 && (reinterpret_cast<uintptr_t>(a.q) & 7) == 0;
+#pragma unroll
+        for (int c = 0; c < NC; c++) {
+            const int32_t col = (c * NT + t) * 8;
+            if (col >= a.width) continue;
+            float o[8];
+            for (int k = 0; k < 8; k++) o[k] = to_range(v[c][k] * inv);
+            int lo = __builtin_amdgcn_cvt_pk_fp8_f32(o[0], o[1], 0, false), hi = __builtin_amdgcn_cvt_pk_fp8_f32(o[4], o[5], 0, false);
+            lo = __builtin_amdgcn_cvt_pk_fp8_f32(o[2], o[3], lo, true);
+            hi = __builtin_amdgcn_cvt_pk_fp8_f32(o[6], o[7], hi, true);
+            uint8_t* p = a.q + row * a.ld_y + col;
+            if (vq) {
+                *reinterpret_cast<u32x2*>(p) = u32x2{(uint32_t)lo, (uint32_t)hi};
+            } else {
+                for (int k = 0; k < 8; k++)
+                    if (col + k < a.width) p[k] = (uint8_t)((uint32_t)(k < 4 ? lo : hi) >> ((k & 3) * 8));
+            }
+        }
+    }
+}
+
+// Each group of NT threads walks rows group, group + groups, ...; its columns' share of dweight stays in
+// registers and leaves once per group.
+template <class T, int NT, int NC>
+__global__ __launch_bounds__(block_of(NT)) void norm_bwd_kernel(NormArgs a, int32_t groups) {
+    __shared__ float lds[16];
+    const int32_t group = blockIdx.x * rows_per_block(NT) + threadIdx.x / NT;
+    const int t = threadIdx.x % NT;
+    if (NT <= 64 && group >= groups) return;
+    const bool vs = vec8(a.s, a.ld_s, a.width, T::type), vy = vec8(a.dy, a.ld_y, a.width, T::type);
+    const bool vr = vec8(a.ds, a.ld_r, a.width, T::type), vx = vec8(a.dx, a.ld_x, a.width, T::type);
+    float w[NC][8], acc[NC][8];
+#pragma unroll
+    for (int c = 0; c < NC; c++) {
+        if (a.w) load8<F32>(a.w, 0, (c * NT + t) * 8, a.width, vec8(a.w, 8, a.width, GS_TYPE_F32), w[c]);
+        for (int k = 0; k < 8; k++) {
+            if (!a.w) w[c][k] = 1.0f;
+            acc[c][k] = 0.0f;
+        }
+    }
+    for (int64_t row = group; row < a.rows; row += groups) {
+        float s[NC][8], g[NC][8], d[NC][8];
+#pragma unroll
+        for (int c = 0; c < NC; c++) {
+            load8<T>(a.s, row * a.ld_s, (c * NT + t) * 8, a.width, vs, s[c]);
+            load8<T>(a.dy, row * a.ld_y, (c * NT + t) * 8, a.width, vy, g[c]);
+            if (a.ds) load8<T>(a.ds, row * a.ld_r, (c * NT + t) * 8, a.width, vr, d[c]);
+        }
+        float sq = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int c = 0; c < NC; c++)
+            for (int k = 0; k < 8; k++) {
+                sq = fmaf(s[c][k], s[c][k], sq);
+                dot = fmaf(g[c][k] * w[c][k], s[c][k], dot);
+            }
+        const float rstd = 1.0f / sqrtf(row_sum<NT>(sq, lds) / (float)a.width + a.eps);
+        const float mean = row_sum<NT>(dot, lds) * rstd / (float)a.width;  // mean of dy weight n
+#pragma unroll
+        for (int c = 0; c < NC; c++) {
+            for (int k = 0; k < 8; k++) {
+                const float n = s[c][k] * rstd;
+                acc[c][k] = fmaf(g[c][k], n, acc[c][k]);
+                const float o = rstd * fmaf(-n, mean, g[c][k] * w[c][k]);
+                g[c][k] = a.ds ? d[c][k] + o : o;
+            }
+            store8<T>(a.dx, row * a.ld_x, (c * NT + t) * 8, a.width, vx, g[c]);
+        }
+    }
+    if (a.partial) {
+#pragma unroll
+        for (int c = 0; c < NC; c++)
+            store8<F32>(a.partial, (int64_t)group * a.width, (c * NT + t) * 8, a.width, (a.width & 7) == 0, acc[c]);
+    }
+}
+
+// Threads per row and chunks per thread by the row's width.
+struct RowShape {
+    int nt, nc;
+};
+RowShape row_shape(int32_t width) {
+    if (width <= 64) return {8, 1};
+    if (width <= 128) return {16, 1};
+    if (width <= 256) return {32, 1};
+    if (width <= 512) return {64, 1};
+    if (width <= 2048) return {64, 4};
+    if (width <= 8192) return {256, 4};
+    return {1024, 4};
+}
+
+template <class T, int NT, int NC>
+hipError_t fwd_one(const NormArgs& a, hipStream_t s) {
+    const int64_t blocks = (a.rows + rows_per_block(NT) - 1) / rows_per_block(NT);
+    hipLaunchKernelGGL((norm_fwd_kernel<T, NT, NC>), dim3((unsigned)blocks), dim3(block_of(NT)), 0, s, a);
+    return hipGetLastError();
+}
+template <class T, int NT, int NC>
+hipError_t bwd_one(const NormArgs& a, int32_t groups, hipStream_t s) {
+    const int blocks = (groups + rows_per_block(NT) - 1) / rows_per_block(NT);
+    hipLaunchKernelGGL((norm_bwd_kernel<T, NT, NC>), dim3((unsigned)blocks), dim3(block_of(NT)), 0, s, a, groups);
+    return hipGetLastError();
+}
+
+template <class T>
+hipError_t fwd_type(const NormArgs& a, hipStream_t s) {
+    const RowShape r = row_shape(a.width);
+    if (r.nt == 8) return fwd_one<T, 8, 1>(a, s);
+    if (r.nt == 16) return fwd_one<T, 16, 1>(a, s);
+    if (r.nt == 32) return fwd_one<T, 32, 1>(a, s);
+    if (r.nt == 64) return r.nc == 1 ? fwd_one<T, 64, 1>(a, s) : fwd_one<T, 64, 4>(a, s);
+    return r.nt == 256 ? fwd_one<T, 256, 4>(a, s) : fwd_one<T, 1024, 4>(a, s);
+}
+template <class T>
+hipError_t bwd_type(const NormArgs& a, int32_t groups, hipStream_t s) {
+    const RowShape r = row_shape(a.width);
+    if (r.nt == 8) return bwd_one<T, 8, 1>(a, groups, s);
+    if (r.nt == 16) return bwd_one<T, 16, 1>(a, groups, s);
+    if (r.nt == 32) return bwd_one<T, 32, 1>(a, groups, s);
+    if (r.nt == 64) return r.nc == 1 ? bwd_one<T, 64, 1>(a, groups, s) : bwd_one<T, 64, 4>(a, groups, s);
+    return r.nt == 256 ? bwd_one<T, 256, 4>(a, groups, s) : bwd_one<T, 1024, 4>(a, groups, s);
+}
+
+// ---- operand copies -------------------------------------------------------------------------------
+// A 64 x 64 block through LDS, so that both the rows' and the columns' side move whole lines whichever
+// of the source's axes is contiguous.
+__global__ __launch_bounds__(256) void pack_kernel(const void* src, int src_type, int64_t s_row, int64_t s_col, int64_t rows,
+                                                   int32_t cols, void* dst, int dst_type, int64_t ld) {
+    __shared__ float tile[64][65];
+    const int64_t r0 = (int64_t)blockIdx.x * 64;
+    const int32_t c0 = blockIdx.y * 64;
+    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+    if (s_col == 1) {
+        for (int k = y; k < 64; k += 4) {
+            const int64_t r = r0 + k;
+            const int32_t c = c0 + x;
+            tile[k][x] = r < rows && c < cols ? load_elem(src, src_type, r * s_row + c) : 0.0f;
+        }
+    } else {
+        for (int k = y; k < 64; k += 4) {
+            const int64_t r = r0 + x;
+            const int32_t c = c0 + k;
+            tile[x][k] = r < rows && c < cols ? load_elem(src, src_type, r * s_row + c * s_col) : 0.0f;
+        }
+    }
+    __syncthreads();
+    for (int k = y; k < 64; k += 4) {
+        const int64_t r = r0 + k;
+        const int32_t c = c0 + x;
+        if (r < rows && c < ld) store_elem(dst, dst_type, r * ld + c, tile[k][x]);
+    }
+}
+// The same for bytes (8-bit operands), rows contiguous on both sides.
+__global__ __launch_bounds__(256) void pack_bytes_kernel(const uint8_t* src, int64_t s_row, int64_t rows, int32_t cols,
+                                                         uint8_t* dst, int64_t ld) {
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        for (int64_t c = threadIdx.x; c < ld; c += 256) dst[r * ld + c] = c < cols ? src[r * s_row + c] : (uint8_t)0;
+}
+
+// ---- column sums ----------------------------------------------------------------------------------
+// Stage 1: 64 columns x one part of the rows per workgroup, four rows at a time; the four sums meet in LDS.
+__global__ __launch_bounds__(256) void colsum_kernel(const void* in, int type, int64_t s_row, int64_t s_col, int64_t rows,
+                                                     int32_t cols, int64_t rows_per_part, float* out) {
+    __shared__ float part[4][64];
+    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+    const int32_t c = blockIdx.x * 64 + x;
+    const int64_t r0 = (int64_t)blockIdx.y * rows_per_part, r1 = r0 + rows_per_part < rows ? r0 + rows_per_part : rows;
+    float s = 0.0f;
+    if (c < cols)
+        for (int64_t r = r0 + y; r < r1; r += 4) s += load_elem(in, type, r * s_row + c * s_col);
+    part[y][x] = s;
+    __syncthreads();
+    if (y == 0 && c < cols) out[(int64_t)blockIdx.y * cols + c] = (part[0][x] + part[1][x]) + (part[2][x] + part[3][x]);
+}
+// Rows along the columns' axis (channel-major input): one part of one column per workgroup.
+__global__ __launch_bounds__(256) void rowsum_kernel(const void* in, int type, int64_t s_col, int64_t rows, int32_t cols,
+                                                     int64_t rows_per_part, float* out) {
+    __shared__ float lds[16];
+    const int64_t r0 = (int64_t)blockIdx.y * rows_per_part, r1 = r0 + rows_per_part < rows ? r0 + rows_per_part : rows;
+    const int64_t base = (int64_t)blockIdx.x * s_col;
+    float s = 0.0f;
+    for (int64_t r = r0 + threadIdx.x; r < r1; r += 256) s += load_elem(in, type, base + r);
+    s = row_sum<256>(s, lds);
+    if (threadIdx.x == 0) out[(int64_t)blockIdx.y * cols + blockIdx.x] = s;
+}
+
+int64_t colsum_parts(int64_t rows) {
+    int64_t p = (rows + 255) / 256;
+    return p < 1 ? 1 : (p > 512 ? 512 : p);
+}
+
+// ---- join of a split product ----------------------------------------------------------------------
+__global__ __launch_bounds__(256) void reduce_kernel(GemmArgs g) {
+    const int64_t per_row = (g.J + 3) / 4, total = per_row * g.I;
+    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < total; n += (int64_t)gridDim.x * 256) {
+        const int32_t i = (int32_t)(n / per_row), j = (int32_t)(n % per_row) * 4;
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const float* p = g.partial + (int64_t)i * g.J + j;
+        for (int s = 0; s < g.splits; s++, p += (int64_t)g.I * g.J)
+            for (int k = 0; k < 4; k++)
+                if (j + k < g.J) v[k] += p[k];
+        for (int k = 0; k < 4; k++) {
+            if (j + k >= g.J) break;
+            float z = v[k];
+            if (g.e.scale_i) z *= g.e.scale_i[i] * g.e.scale_j[j + k];
+            if (g.e.bias) z += g.e.bias[g.e.bias_on_i ? i : j + k];
+            z = act_value(z, g.e.act);
+            if (g.e.res) z += load_elem(g.e.res, g.e.y_type, (int64_t)i * g.e.r_si + (int64_t)(j + k) * g.e.r_sj);
+            store_elem(g.e.y, g.e.y_type, (int64_t)i * g.e.y_si + (int64_t)(j + k) * g.e.y_sj, z);
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_norm_fwd(int type, const NormArgs& a, hipStream_t s) {
+    if (type == GS_TYPE_BF16) return fwd_type<Bf16>(a, s);
+    if (type == GS_TYPE_F16) return fwd_type<F16>(a, s);
+    return fwd_type<F32>(a, s);
+}
+
+// Groups of rows of the backward: enough to fill the card, few enough that their partial sums cost little.
+int32_t norm_groups(int64_t rows, int32_t width) {
+    const RowShape r = row_shape(width);
+    const int64_t most = (int64_t)2048 * rows_per_block(r.nt) / (r.nt >= 256 ? 2 : 1);
+    return (int32_t)(rows < most ? rows : most);
+}
+
+hipError_t launch_norm_bwd(int type, const NormArgs& a, int32_t groups, hipStream_t s) {
+    if (type == GS_TYPE_BF16) return bwd_type<Bf16>(a, groups, s);
+    if (type == GS_TYPE_F16) return bwd_type<F16>(a, groups, s);
+    return bwd_type<F32>(a, groups, s);
+}
+
+hipError_t launch_pack(const void* src, int src_type, int64_t s_row, int64_t s_col, int64_t rows, int32_t cols, void* dst,
+                       int dst_type, int64_t ld_dst, hipStream_t s) {
+    if (rows <= 0) return hipSuccess;
+    if (src_type == GS_TYPE_E4M3) {
+        const unsigned blocks = (unsigned)(rows < 65536 ? rows : 65536);
+        hipLaunchKernelGGL(pack_bytes_kernel, dim3(blocks), dim3(256), 0, s, static_cast<const uint8_t*>(src), s_row, rows,
+                           cols, static_cast<uint8_t*>(dst), ld_dst);
+    } else {
+        hipLaunchKernelGGL(pack_kernel, dim3((unsigned)((rows + 63) / 64), (unsigned)((ld_dst + 63) / 64)), dim3(256), 0, s,
+                           src, src_type, s_row, s_col, rows, cols, dst, dst_type, ld_dst);
+    }
+    return hipGetLastError();
+}
+
+size_t colsum_partial_floats(int64_t rows, int32_t cols) { return (size_t)colsum_parts(rows) * cols; }
+
+hipError_t launch_colsum(const void* in, int type, int64_t s_row, int64_t s_col, int64_t rows, int32_t cols, float* partial,
+                         float* out, hipStream_t s) {
+    const int64_t parts = colsum_parts(rows), per = rows > 0 ? (rows + parts - 1) / parts : 1;
+    float* first = parts > 1 ? partial : out;
+    if (s_row == 1 && s_col != 1)
+        hipLaunchKernelGGL(rowsum_kernel, dim3((unsigned)cols, (unsigned)parts), dim3(256), 0, s, in, type, s_col, rows, cols,
+                           per, first);
+    else
+        hipLaunchKernelGGL(colsum_kernel, dim3((unsigned)((cols + 63) / 64), (unsigned)parts), dim3(256), 0, s, in, type,
+                           s_row, s_col, rows, cols, per, first);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || parts == 1) return e;
+    hipLaunchKernelGGL(colsum_kernel, dim3((unsigned)((cols + 63) / 64), 1), dim3(256), 0, s, partial, GS_TYPE_F32, (int64_t)cols,
+                       (int64_t)1, parts, cols, parts, out);
+    return hipGetLastError();
+}
+
+hipError_t launch_gemm(int type, TileShape shape, Layout la, Layout lb, EpiKind kind, const GemmArgs& g, hipStream_t s) {
+    if (type == GS_TYPE_BF16) return launch_gemm_bf16(shape, la, lb, kind, g, s);
+    if (type == GS_TYPE_F16) return launch_gemm_f16(shape, la, lb, kind, g, s);
+    return launch_gemm_e4m3(shape, la, lb, kind, g, s);
+}
+
+hipError_t launch_few_rows(int type, EpiKind kind, bool aligned, const GemmArgs& g, hipStream_t s) {
+    if (type == GS_TYPE_BF16) return launch_few_rows_bf16(kind, aligned, g, s);
+    if (type == GS_TYPE_F16) return launch_few_rows_f16(kind, aligned, g, s);
+    return launch_few_rows_e4m3(kind, aligned, g, s);
+}
+
+hipError_t launch_gemm_reduce(const GemmArgs& g, hipStream_t s) {
+    const int64_t total = ((int64_t)g.J + 3) / 4 * g.I;
+    int64_t blocks = (total + 255) / 256;
+    if (blocks > 8192) blocks = 8192;
+    hipLaunchKernelGGL(reduce_kernel, dim3((unsigned)blocks), dim3(256), 0, s, g);
+    return hipGetLastError();
+}
+
+}  // namespace gsmi

@@ -84,6 +84,23 @@ class gs_adam_params(ctypes.Structure):
     _fields_ = [("beta1", ctypes.c_float), ("beta2", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
+class gs_norm_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("width", ctypes.c_int32), ("type", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("ld_x", ctypes.c_int64), ("ld_r", ctypes.c_int64), ("ld_s", ctypes.c_int64), ("ld_y", ctypes.c_int64)]
+
+
+class gs_linear_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("in_", ctypes.c_int32), ("out", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("y_type", ctypes.c_int32), ("grad_type", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("y_channel_major", ctypes.c_int32), ("ld_x", ctypes.c_int64), ("ld_w", ctypes.c_int64),
+                ("ld_y", ctypes.c_int64), ("ld_r", ctypes.c_int64)]
+
+
+GS_TYPE_F32, GS_TYPE_BF16, GS_TYPE_F16, GS_TYPE_E4M3 = range(4)
+GS_ACT_NONE, GS_ACT_RELU, GS_ACT_SILU, GS_ACT_GELU = range(4)
+GS_NORM_MAX_WIDTH = 32768
+GS_LINEAR_MAX_WIDTH = 1048576
+
 _P = ctypes.POINTER
 _SIGS = {
     "gs_version": (ctypes.c_char_p, []),
@@ -141,6 +158,18 @@ _SIGS = {
                                          ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "gs_adam_flush": (ctypes.c_int, [ctypes.c_int32, _P(gs_adam_group), ctypes.c_int32, _P(gs_adam_params),
                                      ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]),
+    "gs_rmsnorm": (ctypes.c_int, [_P(gs_norm_desc)] + [ctypes.c_void_p] * 8),
+    "gs_quantize_rows": (ctypes.c_int, [_P(gs_norm_desc)] + [ctypes.c_void_p] * 4),
+    "gs_rmsnorm_bwd_workspace_size": (ctypes.c_size_t, [_P(gs_norm_desc)]),
+    "gs_rmsnorm_bwd": (ctypes.c_int, [_P(gs_norm_desc)] + [ctypes.c_void_p] * 7 + [ctypes.c_size_t, ctypes.c_void_p]),
+    "gs_linear_workspace_size": (ctypes.c_size_t, [_P(gs_linear_desc)]),
+    "gs_linear": (ctypes.c_int, [_P(gs_linear_desc)] + [ctypes.c_void_p] * 8 + [ctypes.c_size_t, ctypes.c_void_p]),
+    "gs_linear_bwd_workspace_size": (ctypes.c_size_t, [_P(gs_linear_desc)]),
+    "gs_linear_bwd": (ctypes.c_int, [_P(gs_linear_desc)] + [ctypes.c_void_p] * 8 + [ctypes.c_size_t, ctypes.c_void_p]),
+    "gs_gated_workspace_size": (ctypes.c_size_t, [_P(gs_linear_desc)]),
+    "gs_gated": (ctypes.c_int, [_P(gs_linear_desc)] + [ctypes.c_void_p] * 7 + [ctypes.c_size_t, ctypes.c_void_p]),
+    "gs_gated_bwd_workspace_size": (ctypes.c_size_t, [_P(gs_linear_desc)]),
+    "gs_gated_bwd": (ctypes.c_int, [_P(gs_linear_desc)] + [ctypes.c_void_p] * 8 + [ctypes.c_size_t, ctypes.c_void_p]),
 }
 
 _lib = None
@@ -371,3 +400,58 @@ def gs_adam_step_seen(n, groups, hp: gs_adam_params, t, last_step, seen, stream=
 def gs_adam_flush(n, groups, hp: gs_adam_params, t, last_step, stream=None):
     _check(load().gs_adam_flush(n, groups, len(groups), ctypes.byref(hp), int(t), _ptr(last_step), _stream(stream)),
            "gs_adam_flush")
+
+
+# The neural decoder's operators take device addresses (or None), as the C ABI does: their callers
+# (neural.py) keep strided rows, which _ptr() refuses.
+def gs_rmsnorm(desc: gs_norm_desc, x, residual, weight, s, y, q, q_scale, stream=None):
+    _check(load().gs_rmsnorm(ctypes.byref(desc), x, residual, weight, s, y, q, q_scale, _stream(stream)), "gs_rmsnorm")
+
+
+def gs_quantize_rows(desc: gs_norm_desc, x, q, q_scale, stream=None):
+    _check(load().gs_quantize_rows(ctypes.byref(desc), x, q, q_scale, _stream(stream)), "gs_quantize_rows")
+
+
+def gs_rmsnorm_bwd_workspace_size(desc: gs_norm_desc) -> int:
+    return int(load().gs_rmsnorm_bwd_workspace_size(ctypes.byref(desc)))
+
+
+def gs_rmsnorm_bwd(desc: gs_norm_desc, s, weight, dy, ds, dx, dweight, ws, ws_bytes, stream=None):
+    _check(load().gs_rmsnorm_bwd(ctypes.byref(desc), s, weight, dy, ds, dx, dweight, ws, ws_bytes, _stream(stream)),
+           "gs_rmsnorm_bwd")
+
+
+def gs_linear_workspace_size(desc: gs_linear_desc) -> int:
+    return int(load().gs_linear_workspace_size(ctypes.byref(desc)))
+
+
+def gs_linear(desc: gs_linear_desc, x, x_scale, weight, w_scale, bias, residual, y, ws, ws_bytes, stream=None):
+    _check(load().gs_linear(ctypes.byref(desc), x, x_scale, weight, w_scale, bias, residual, y, ws, ws_bytes,
+                            _stream(stream)), "gs_linear")
+
+
+def gs_linear_bwd_workspace_size(desc: gs_linear_desc) -> int:
+    return int(load().gs_linear_bwd_workspace_size(ctypes.byref(desc)))
+
+
+def gs_linear_bwd(desc: gs_linear_desc, x, weight, bias, dy, dx, dweight, dbias, ws, ws_bytes, stream=None):
+    _check(load().gs_linear_bwd(ctypes.byref(desc), x, weight, bias, dy, dx, dweight, dbias, ws, ws_bytes,
+                                _stream(stream)), "gs_linear_bwd")
+
+
+def gs_gated_workspace_size(desc: gs_linear_desc) -> int:
+    return int(load().gs_gated_workspace_size(ctypes.byref(desc)))
+
+
+def gs_gated(desc: gs_linear_desc, x, x_scale, weight, w_scale, bias, h, ws, ws_bytes, stream=None):
+    _check(load().gs_gated(ctypes.byref(desc), x, x_scale, weight, w_scale, bias, h, ws, ws_bytes, _stream(stream)),
+           "gs_gated")
+
+
+def gs_gated_bwd_workspace_size(desc: gs_linear_desc) -> int:
+    return int(load().gs_gated_bwd_workspace_size(ctypes.byref(desc)))
+
+
+def gs_gated_bwd(desc: gs_linear_desc, x, weight, bias, dh, dx, dweight, dbias, ws, ws_bytes, stream=None):
+    _check(load().gs_gated_bwd(ctypes.byref(desc), x, weight, bias, dh, dx, dweight, dbias, ws, ws_bytes,
+                               _stream(stream)), "gs_gated_bwd")

@@ -1,0 +1,218 @@
+"""Plans of the neural parameter decoder's operators (gs_rmsnorm, gs_linear, gs_gated): each plan owns
+its output buffers and workspace, allocated once for a number of rows, and marshals arguments.
+
+A plan's outputs are its own buffers: the next call of the same method overwrites them.  Row arrays may
+be views with a row stride (the last axis contiguous); vectors are float32.  Work goes to torch's
+current stream, or to the `stream` argument.  Nothing here computes any part of an operator.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import gsmi
+
+TYPES = {torch.float32: gsmi.GS_TYPE_F32, torch.bfloat16: gsmi.GS_TYPE_BF16, torch.float16: gsmi.GS_TYPE_F16,
+         torch.float8_e4m3fn: gsmi.GS_TYPE_E4M3}
+ACTS = {"none": gsmi.GS_ACT_NONE, "relu": gsmi.GS_ACT_RELU, "silu": gsmi.GS_ACT_SILU, "gelu": gsmi.GS_ACT_GELU}
+
+
+def _rows(t, name: str, rows: int, width: int, dtype):
+    """(address, row stride) of a rows x width view."""
+    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
+        raise ValueError(f"{name}: expected {dtype} [{rows}, {width}], got {t.dtype} {list(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: device tensor expected")
+    step, across = t.stride()
+    if across != 1 and width > 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    if rows > 1 and step < width:
+        raise ValueError(f"{name}: rows overlap (stride {step}, width {width})")
+    return t.data_ptr(), (step if rows > 1 else width)
+
+
+def _vector(t, name: str, n: int):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name}: expected torch.float32 [{n}], got {t.dtype} {list(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous device tensor expected")
+    return t.data_ptr()
+
+
+def _aligned(t):
+    """The products' operands start at a multiple of 16 bytes: a view that does not is copied."""
+    return t if t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+
+
+class RmsNorm:
+    """s = x + residual, y = s / sqrt(mean(s^2) + eps) * weight over the rows of [rows, width];
+    quantize: y leaves as 8-bit rows q with a scale each, y ~ q * scale[:, None]."""
+
+    def __init__(self, rows: int, width: int, dtype, eps: float = 1e-6, quantize: bool = False, device="cuda"):
+        self.rows, self.width, self.dtype, self.quantize = rows, width, dtype, quantize
+        self.device = torch.device(device)
+        self.desc = gsmi.gs_norm_desc(rows, width, TYPES[dtype], eps, 0, 0, 0, 0)
+        self._fwd = self._bwd = None
+
+    def _empty(self, *shape, dtype=None):
+        return torch.empty(*shape, dtype=dtype or self.dtype, device=self.device)
+
+    def forward(self, x, weight=None, residual=None, stream=None):
+        """(s, y), or (s, q, scale) with quantize.  Without a residual s is x itself."""
+        m, d = self.rows, self.width
+        if self._fwd is None:
+            s = self._empty(m, d)
+            self._fwd = (s, self._empty(m, d, dtype=torch.float8_e4m3fn), self._empty(m, dtype=torch.float32)) \
+                if self.quantize else (s, self._empty(m, d))
+        c = self.desc
+        c.ld_s = c.ld_y = d
+        px, c.ld_x = _rows(x, "x", m, d, self.dtype)
+        pr = None
+        if residual is not None:
+            pr, c.ld_r = _rows(residual, "residual", m, d, self.dtype)
+        out = self._fwd
+        ps = out[0].data_ptr() if residual is not None else None
+        pw = _vector(weight, "weight", d)
+        if self.quantize:
+            gsmi.gs_rmsnorm(c, px, pr, pw, ps, None, out[1].data_ptr(), out[2].data_ptr(), stream)
+        else:
+            gsmi.gs_rmsnorm(c, px, pr, pw, ps, out[1].data_ptr(), None, None, stream)
+        return out if residual is not None else (x,) + out[1:]
+
+    def backward(self, s, weight, dy, ds=None, stream=None):
+        """(dx, dweight): dx is the gradient of x and of the residual; ds the one that reaches s past
+        the norm.  dweight is None without a weight."""
+        m, d = self.rows, self.width
+        if self._bwd is None:
+            self._bwd = (self._empty(m, d), self._empty(d, dtype=torch.float32),
+                         self._empty(max(1, gsmi.gs_rmsnorm_bwd_workspace_size(self.desc)), dtype=torch.uint8))
+        dx, dw, ws = self._bwd
+        c = self.desc
+        c.ld_x = d
+        p_s, c.ld_s = _rows(s, "s", m, d, self.dtype)
+        p_dy, c.ld_y = _rows(dy, "dy", m, d, self.dtype)
+        p_ds = None
+        if ds is not None:
+            p_ds, c.ld_r = _rows(ds, "ds", m, d, self.dtype)
+        pw = _vector(weight, "weight", d)
+        gsmi.gs_rmsnorm_bwd(c, p_s, pw, p_dy, p_ds, dx.data_ptr(), dw.data_ptr() if pw else None, ws.data_ptr(),
+                            ws.numel(), stream)
+        return dx, (dw if pw else None)
+
+
+def quantize_rows(x, stream=None):
+    """(q, scale): rows of x [rows, width] in 8 bits with a scale each, x ~ q * scale[:, None]."""
+    rows, width = x.shape
+    c = gsmi.gs_norm_desc(rows, width, TYPES[x.dtype], 0.0, 0, 0, 0, 0)
+    px, c.ld_x = _rows(x, "x", rows, width, x.dtype)
+    q = torch.empty(rows, width, dtype=torch.float8_e4m3fn, device=x.device)
+    scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    gsmi.gs_quantize_rows(c, px, q.data_ptr(), scale.data_ptr(), stream)
+    return q, scale
+
+
+class _Product:
+    def __init__(self, rows, n_in, n_out, dtype, act, y_dtype, channel_major, grad_dtype, backward, device, gated):
+        self.rows, self.n_in, self.n_out, self.gated = rows, n_in, n_out, gated
+        self.w_rows = 2 * n_out if gated else n_out
+        self.dtype = dtype
+        self.y_dtype = y_dtype or (torch.bfloat16 if dtype == torch.float8_e4m3fn else dtype)
+        self.grad_dtype = grad_dtype or dtype
+        self.channel_major = channel_major
+        self.device = torch.device(device)
+        self.desc = gsmi.gs_linear_desc(rows, n_in, n_out, TYPES[dtype], TYPES[self.y_dtype], TYPES[self.grad_dtype],
+                                        ACTS[act], int(channel_major), n_in, n_in, 0, 0)
+        self.ws = None
+        self._y = self._grads = None
+        self._reserve(backward)
+
+    def _reserve(self, backward: bool):
+        """A workspace for the strides in the descriptor (a view's strides can ask for more)."""
+        size = getattr(gsmi, ("gs_gated" if self.gated else "gs_linear") + ("_bwd" if backward else "") + "_workspace_size")
+        need = size(self.desc)
+        if need and (self.ws is None or self.ws.numel() < need):
+            self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+
+    def _ws(self):
+        return (None, 0) if self.ws is None else (self.ws.data_ptr(), self.ws.numel())
+
+    @property
+    def _y_shape(self):
+        return (self.n_out, self.rows) if self.channel_major else (self.rows, self.n_out)
+
+    def _operands(self, x, weight, backward):
+        c, seen = self.desc, (self.desc.ld_x, self.desc.ld_w)
+        x, weight = _aligned(x), _aligned(weight)
+        px, c.ld_x = _rows(x, "x", self.rows, self.n_in, self.dtype)
+        pw, c.ld_w = _rows(weight, "weight", self.w_rows, self.n_in, self.dtype)
+        if (c.ld_x, c.ld_w) != seen or backward:
+            self._reserve(backward)
+        return x, weight, px, pw
+
+    def _forward(self, x, weight, bias, residual, x_scale, w_scale, out, stream):
+        c = self.desc
+        c.ld_y = c.ld_r = 0
+        x, weight, px, pw = self._operands(x, weight, False)
+        pb = _vector(bias, "bias", self.w_rows)
+        sx, sw = _vector(x_scale, "x_scale", self.rows), _vector(w_scale, "w_scale", self.w_rows)
+        if out is None:
+            if self._y is None:
+                self._y = torch.empty(*self._y_shape, dtype=self.y_dtype, device=self.device)
+            out = self._y
+        py, c.ld_y = _rows(out, "out", *self._y_shape, self.y_dtype)
+        if self.gated:
+            gsmi.gs_gated(c, px, sx, pw, sw, pb, py, *self._ws(), stream)
+            return out
+        pr = None
+        if residual is not None:
+            pr, c.ld_r = _rows(residual, "residual", *self._y_shape, self.y_dtype)
+        gsmi.gs_linear(c, px, sx, pw, sw, pb, pr, py, *self._ws(), stream)
+        return out
+
+    def backward(self, x, weight, dy, bias=None, stream=None):
+        """(dx, dweight, dbias) from the gradient of the result; dbias is None without a bias.  bias is
+        the forward's: it belongs to the pre-activation that the backward computes again."""
+        c = self.desc
+        c.ld_r = 0
+        dy = _aligned(dy)
+        p_dy, c.ld_y = _rows(dy, "dy", *self._y_shape, self.y_dtype)
+        x, weight, px, pw = self._operands(x, weight, True)
+        pb = _vector(bias, "bias", self.w_rows)
+        if self._grads is None:
+            self._grads = (torch.empty(self.rows, self.n_in, dtype=self.dtype, device=self.device),
+                           torch.empty(self.w_rows, self.n_in, dtype=self.grad_dtype, device=self.device),
+                           torch.empty(self.w_rows, dtype=torch.float32, device=self.device))
+        dx, dw, db = self._grads
+        c.ld_r = self.n_in
+        call = gsmi.gs_gated_bwd if self.gated else gsmi.gs_linear_bwd
+        call(c, px, pw, pb, p_dy, dx.data_ptr(), dw.data_ptr(), db.data_ptr() if pb else None, *self._ws(), stream)
+        return dx, dw, (db if pb else None)
+
+
+class Linear(_Product):
+    """y = act(x weight^T + bias) + residual; x [rows, in], weight [out, in], y [rows, out], or
+    [out, rows] with channel_major (the layout of gs_gaussians; also of residual and dy).  act: "none",
+    "relu", "silu" or "gelu".  8-bit operands (torch.float8_e4m3fn) come with x_scale [rows] and
+    w_scale [out] and have no backward.  backward: reserve the backward's workspace at once."""
+
+    def __init__(self, rows: int, in_features: int, out_features: int, dtype, act: str = "none", y_dtype=None,
+                 channel_major: bool = False, grad_dtype=None, backward: bool = False, device="cuda"):
+        super().__init__(rows, in_features, out_features, dtype, act, y_dtype, channel_major, grad_dtype, backward,
+                         device, False)
+
+    def forward(self, x, weight, bias=None, residual=None, x_scale=None, w_scale=None, out=None, stream=None):
+        """y in the plan's buffer, or in `out` (which may be the residual)."""
+        return self._forward(x, weight, bias, residual, x_scale, w_scale, out, stream)
+
+
+class GatedUnit(_Product):
+    """h = act(x Wg^T + bg) * (x Wu^T + bu); weight [2 hidden, in] holds Wg above Wu, bias [2 hidden];
+    h [rows, hidden].  The backward computes both projections again from x."""
+
+    def __init__(self, rows: int, in_features: int, hidden: int, dtype, act: str = "silu", y_dtype=None, grad_dtype=None,
+                 backward: bool = False, device="cuda"):
+        super().__init__(rows, in_features, hidden, dtype, act, y_dtype, False, grad_dtype, backward, device, True)
+
+    def forward(self, x, weight, bias=None, x_scale=None, w_scale=None, out=None, stream=None):
+        return self._forward(x, weight, bias, None, x_scale, w_scale, out, stream)

@@ -525,6 +525,136 @@ gs_status gs_adam_step_seen(int32_t n, const gs_adam_group* groups, int32_t n_gr
 gs_status gs_adam_flush(int32_t n, const gs_adam_group* groups, int32_t n_groups, const gs_adam_params* hp,
                         int32_t t, int32_t* last_step, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Neural parameter decoder: the operators of a small network that predicts the parameters of the
+ * Gaussians from features (one row per Gaussian, or per token of a network that emits Gaussians):
+ * the root-mean-square norm with the residual's addition, a linear map with bias, activation and
+ * residual in its epilogue, and the gated feed-forward unit, each with its backward.  Sums, norm
+ * statistics and everything between a load and a store are float32; products run on the matrix
+ * units.  Results do not depend on atomics: equal calls give equal bits.
+ *
+ * Rows are stored along memory: element (r, c) of an array with row stride ld at r * ld + c.  A row
+ * stride of 0 in a descriptor means contiguous rows.  x, weight and the gradients' operands (x, weight,
+ * dy, dh) must be 16-byte aligned; other arrays are aligned to their element.  Strides that are no
+ * multiple of 16 bytes are served (through a copy in the workspace where a product needs it).
+ * rows == 0 is valid: forward calls do nothing, backward calls set the weight gradients to zero.
+ * ------------------------------------------------------------------------------------------ */
+typedef enum {
+    GS_TYPE_F32 = 0,
+    GS_TYPE_BF16 = 1,
+    GS_TYPE_F16 = 2,
+    GS_TYPE_E4M3 = 3, /* 8-bit float, 4 exponent and 3 mantissa bits, largest value 448, no infinity */
+    GS_TYPE_FORCE_INT32 = 0x7FFFFFFF
+} gs_type;
+
+typedef enum {
+    GS_ACT_NONE = 0,
+    GS_ACT_RELU = 1, /* derivative 0 at 0; NaN stays NaN */
+    GS_ACT_SILU = 2, /* z / (1 + e^-z) */
+    GS_ACT_GELU = 3, /* z Phi(z), Phi the standard normal distribution function */
+    GS_ACT_FORCE_INT32 = 0x7FFFFFFF
+} gs_act;
+
+#define GS_NORM_MAX_WIDTH 32768
+
+typedef struct {
+    int32_t rows, width;  /* 1 <= width <= GS_NORM_MAX_WIDTH */
+    int32_t type;         /* of every row array: GS_TYPE_F32, GS_TYPE_BF16 or GS_TYPE_F16 */
+    float eps;            /* finite, >= 0; added to the mean square */
+    int64_t ld_x;         /* row strides in elements (0: width): of x, and of dx in the backward */
+    int64_t ld_r;         /* of the residual, and of ds in the backward */
+    int64_t ld_s;         /* of the sum */
+    int64_t ld_y;         /* of y or q, and of dy in the backward */
+} gs_norm_desc;
+
+/*
+ * gs_rmsnorm: per row, s = x + residual (s = x when residual is NULL), n = s / sqrt(mean(s^2) + eps),
+ * y = n * weight.  The statistics and y come from the unrounded float32 sum.  Outputs, each optional
+ * (at least one given): s in `type`; y in `type`; q and q_scale (both or neither), the row in 8 bits:
+ * q_scale[r] = max|y| / 448 (float32) and q = y / q_scale rounded to GS_TYPE_E4M3, so that
+ * y ~ q * q_scale; a row whose largest magnitude is below 1e-30 has scale 0 and q 0.  weight: float32 [width], NULL for ones.
+ * s may alias x or residual, and y may alias x, when their strides agree (a row is read before it
+ * is written).
+ */
+gs_status gs_rmsnorm(const gs_norm_desc* d, const void* x, const void* residual, const float* weight, void* s,
+                     void* y, void* q, float* q_scale, void* stream);
+
+/* Rows as they are, in 8 bits with a scale each (q and q_scale of gs_rmsnorm for y = x): how weights
+ * and features without a norm become operands of an 8-bit product.  eps is not used. */
+gs_status gs_quantize_rows(const gs_norm_desc* d, const void* x, void* q, float* q_scale, void* stream);
+
+/*
+ * gs_rmsnorm_bwd: from the stored sum s and the gradients dy of y and ds of s (ds may be NULL: none
+ * but through y), with n as above computed again from s:
+ *   dx[r]      = ds[r] + (dy[r] weight - n[r] mean(dy[r] weight n[r])) / sqrt(mean(s[r]^2) + eps),
+ *   dweight    = sum over rows of dy[r] n[r]   (float32 [width]; may be NULL).
+ * dx is the gradient of x and of the residual alike; it may alias dy or ds when the strides agree.
+ * ws: gs_rmsnorm_bwd_workspace_size(d) bytes or more, 256-byte aligned.
+ */
+size_t gs_rmsnorm_bwd_workspace_size(const gs_norm_desc* d);
+gs_status gs_rmsnorm_bwd(const gs_norm_desc* d, const void* s, const float* weight, const void* dy, const void* ds,
+                         void* dx, float* dweight, void* ws, size_t ws_bytes, void* stream);
+
+#define GS_LINEAR_MAX_WIDTH 1048576
+
+typedef struct {
+    int32_t rows;            /* rows of x */
+    int32_t in, out;         /* 1 <= in, out <= GS_LINEAR_MAX_WIDTH; gs_gated: out = hidden units */
+    int32_t type;            /* of x and weight: GS_TYPE_BF16, GS_TYPE_F16 or (forward) GS_TYPE_E4M3 */
+    int32_t y_type;          /* of y, residual and dy / h and dh: GS_TYPE_BF16, GS_TYPE_F16, GS_TYPE_F32 */
+    int32_t grad_type;       /* of dweight: `type` or GS_TYPE_F32 (its operand dz is rounded to `type`) */
+    int32_t act;             /* gs_act */
+    int32_t y_channel_major; /* 0: y[r * ld_y + c]; 1: y[c * ld_y + r], ld_y >= rows: the layout of
+                                gs_gaussians (gs_linear only; also of residual and dy) */
+    int64_t ld_x;            /* row strides in elements (0: contiguous); below 2^21 for x and weight */
+    int64_t ld_w;
+    int64_t ld_y;
+    int64_t ld_r;            /* of residual, and of dx in the backward */
+} gs_linear_desc;
+
+/*
+ * gs_linear: y = act(x weight^T + bias) + residual.  weight [out][in]; bias float32 [out] or NULL;
+ * residual laid out as y (with ld_r) or NULL, and may be y itself.  With type GS_TYPE_E4M3 x_scale
+ * (float32 [rows]) and w_scale (float32 [out]) are required, x and weight stand for x * x_scale and
+ * weight * w_scale row by row; otherwise both are NULL.  ws: gs_linear_workspace_size(d) bytes or
+ * more, 256-byte aligned (NULL when that is 0).
+ */
+size_t gs_linear_workspace_size(const gs_linear_desc* d);
+gs_status gs_linear(const gs_linear_desc* d, const void* x, const float* x_scale, const void* weight,
+                    const float* w_scale, const float* bias, const void* residual, void* y, void* ws,
+                    size_t ws_bytes, void* stream);
+
+/*
+ * gs_linear_bwd: from dy, with dz = dy act'(z) (z is computed again from x where act needs it, and dz is
+ * rounded to `type`, the operand type of the two products that follow):
+ *   dx = dz weight (in `type`, stride ld_r, or NULL), dweight = dz^T x (in grad_type, [out][in]
+ *   contiguous, or NULL), dbias = sum over rows of the unrounded dz (float32 [out], or NULL).
+ * The residual's gradient is dy itself.  bias is the forward's (NULL if it had none).
+ * GS_TYPE_E4M3 has no backward (GS_ERR_UNSUPPORTED).
+ */
+size_t gs_linear_bwd_workspace_size(const gs_linear_desc* d);
+gs_status gs_linear_bwd(const gs_linear_desc* d, const void* x, const void* weight, const float* bias, const void* dy,
+                        void* dx, void* dweight, float* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * gs_gated: h = act(x Wg^T + bg) * (x Wu^T + bu): both projections, the activation and the product in
+ * one kernel.  weight [2 * out][in] holds Wg above Wu; bias float32 [2 * out] or NULL; w_scale (with
+ * GS_TYPE_E4M3) [2 * out]; h [rows][out] in y_type with stride ld_y.  2 * out * ld_w < 2^29.
+ */
+size_t gs_gated_workspace_size(const gs_linear_desc* d);
+gs_status gs_gated(const gs_linear_desc* d, const void* x, const float* x_scale, const void* weight,
+                   const float* w_scale, const float* bias, void* h, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * gs_gated_bwd: from dh.  g and u, the two projections, are computed again from x (nothing is kept
+ * between the passes); dg = dh u act'(g), du = dh act(g), rounded to `type`; dx = [dg du] weight,
+ * dweight = [dg du]^T x ([2 * out][in] contiguous, grad_type), dbias = their sums over rows, unrounded
+ * (float32 [2 * out]).  dx, dweight and dbias may each be NULL.
+ */
+size_t gs_gated_bwd_workspace_size(const gs_linear_desc* d);
+gs_status gs_gated_bwd(const gs_linear_desc* d, const void* x, const void* weight, const float* bias, const void* dh,
+                       void* dx, void* dweight, float* dbias, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
