@@ -97,43 +97,115 @@ __device__ __forceinline__ void epi_gated(const Epi& e, f32x4 gate, f32x4 up, in
     for (int k = 0; k < 4; k++) v[k] = act_value(g[k], e.act) * u[k];
     epi_store(e, i, j, J, v);
 }
-// dz = dy act'(z); returned for the column sums.
-__device__ __forceinline__ f32x4 epi_dz(const Epi& e, f32x4 acc, int32_t i, int32_t j, int32_t J) {
-    const f32x4 z = epi_pre(e, acc, i, j, J, 0), dy = epi_load(e.dy, e.dy_type, e.d_si, e.d_sj, i, j, J);
-    f32x4 o;
-    for (int k = 0; k < 4; k++) {
-        float v, d;
-        act_both(z[k], e.act, v, d);
-        o[k] = j + k < J ? dy[k] * d : 0.0f;
-    }
-    epi_store(e, i, j, J, o);
-    return o;
+// ---- the tiled product's epilogue: eight neighbours along j of row i, read back from LDS ----
+__device__ __forceinline__ bool vec8(const void* p, int type, int64_t si, int64_t sj) {
+    return sj == 1 && (si & (type == GS_TYPE_F32 ? 3 : 7)) == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
 }
-// Gradients of the gate and the up, stored at columns j and J + j.
-__device__ __forceinline__ void epi_dgated(const Epi& e, f32x4 gate, f32x4 up, int32_t i, int32_t j, int32_t J, f32x4& dg, f32x4& du) {
-    const f32x4 g = epi_pre(e, gate, i, j, J, 0), u = epi_pre(e, up, i, j, J, J);
-    const f32x4 dh = epi_load(e.dy, e.dy_type, e.d_si, e.d_sj, i, j, J);
-    for (int k = 0; k < 4; k++) {
-        float v, d;
-        act_both(g[k], e.act, v, d);
-        const bool in = j + k < J;
-        dg[k] = in ? dh[k] * u[k] * d : 0.0f;
-        du[k] = in ? dh[k] * v : 0.0f;
-    }
-    Epi f = e;
-    f.y_pad = 0;
-    epi_store(f, i, j, J, dg);
-    // the ups' columns, with the padding of the whole row after the last of them
-    const int64_t at = (int64_t)i * e.y_si;
-    const int32_t end = e.y_pad > 2 * J ? e.y_pad : 2 * J;
-    if ((J & 3) == 0 && (e.y_si & 3) == 0 && j + 4 <= J && (reinterpret_cast<uintptr_t>(e.y) & 15) == 0) {
-        store_elem4(e.y, e.y_type, at + J + j, du);
+__device__ __forceinline__ void load8(const void* p, int type, int64_t at, int64_t sj, int32_t n, bool vec, float (&v)[8]) {
+    if (vec && n >= 8) {
+        const f32x4 a = load_elem4(p, type, at), b = load_elem4(p, type, at + 4);
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            v[k] = a[k];
+            v[4 + k] = b[k];
+        }
     } else {
-        for (int k = 0; k < 4; k++)
-            if (j + k < J) store_elem(e.y, e.y_type, at + J + j + k, du[k]);
+#pragma unroll
+        for (int k = 0; k < 8; k++) v[k] = k < n ? load_elem(p, type, at + k * sj) : 0.0f;
     }
-    if (j + 4 >= J)
-        for (int32_t c = 2 * J; c < end; c++) store_elem(e.y, e.y_type, at + c, 0.0f);
+}
+// n of the eight values, zeros from there to `end`.
+__device__ __forceinline__ void store8(void* p, int type, int64_t at, int64_t sj, int32_t n, int32_t end, bool vec, const float (&v)[8]) {
+    if (vec && end >= 8) {
+        float o[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++) o[k] = k < n ? v[k] : 0.0f;
+        if (type == GS_TYPE_F32) {
+            f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(p) + at);
+            q[0] = f32x4{o[0], o[1], o[2], o[3]};
+            q[1] = f32x4{o[4], o[5], o[6], o[7]};
+        } else {
+            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + at) =
+                u32x4{pack2(o[0], o[1], type), pack2(o[2], o[3], type), pack2(o[4], o[5], type), pack2(o[6], o[7], type)};
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            if (k < end) store_elem(p, type, at + k * sj, k < n ? v[k] : 0.0f);
+    }
+}
+// scale and bias; shift: the columns' offset in scale_j and bias (the ups have J)
+__device__ __forceinline__ void pre8(const Epi& e, float (&v)[8], int32_t i, int32_t j, int32_t n, int32_t shift) {
+    if (e.scale_i) {
+        const float si = e.scale_i[i];
+#pragma unroll
+        for (int k = 0; k < 8; k++) v[k] *= k < n ? si * e.scale_j[shift + j + k] : 0.0f;
+    }
+    if (e.bias) {
+        const float bi = e.bias_on_i ? e.bias[i] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; k++) v[k] += e.bias_on_i ? bi : (k < n ? e.bias[shift + j + k] : 0.0f);
+    }
+}
+
+// v: the sums of row i, columns j.. (of the gates); u: of the ups.  s0, s1 collect the column sums.
+template <int EPI>
+__device__ __forceinline__ void epi8(const GemmArgs& g, float (&v)[8], float (&u)[8], int32_t i, int32_t j, bool vy, bool vd, bool vr,
+                                     float (&s0)[8], float (&s1)[8]) {
+    const Epi& e = g.e;
+    const int32_t n = g.J - j < 8 ? g.J - j : 8;
+    const int64_t at = (int64_t)i * e.y_si + (int64_t)j * e.y_sj;
+    const int32_t end = e.y_pad > g.J ? (e.y_pad - j < 8 ? e.y_pad - j : 8) : n;
+    pre8(e, v, i, j, n, 0);
+    if (EPI == kEpiLinear) {
+        if (e.act != GS_ACT_NONE) {
+#pragma unroll
+            for (int k = 0; k < 8; k++) v[k] = act_value(v[k], e.act);
+        }
+        if (e.res) {
+            float r[8];
+            load8(e.res, e.y_type, (int64_t)i * e.r_si + (int64_t)j * e.r_sj, e.r_sj, n, vr, r);
+#pragma unroll
+            for (int k = 0; k < 8; k++) v[k] += r[k];
+        }
+        store8(e.y, e.y_type, at, e.y_sj, n, end, vy, v);
+    } else if (EPI == kEpiGated) {
+        pre8(e, u, i, j, n, g.J);
+#pragma unroll
+        for (int k = 0; k < 8; k++) v[k] = act_value(v[k], e.act) * u[k];
+        store8(e.y, e.y_type, at, e.y_sj, n, n, vy, v);
+    } else {
+        float d[8];
+        load8(e.dy, e.dy_type, (int64_t)i * e.d_si + (int64_t)j * e.d_sj, e.d_sj, n, vd, d);
+        if (EPI == kEpiDz) {  // dz = dy act'(z)
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                float a, da;
+                act_both(v[k], e.act, a, da);
+                v[k] = k < n ? d[k] * da : 0.0f;
+                s0[k] += v[k];
+            }
+            store8(e.y, e.y_type, at, e.y_sj, n, end, vy, v);
+        } else {  // dgate = dh up act'(gate) at column j, dup = dh act(gate) at column J + j
+            pre8(e, u, i, j, n, g.J);
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                float a, da;
+                act_both(v[k], e.act, a, da);
+                const float up = u[k];
+                v[k] = k < n ? d[k] * up * da : 0.0f;
+                u[k] = k < n ? d[k] * a : 0.0f;
+                s0[k] += v[k];
+                s1[k] += u[k];
+            }
+            store8(e.y, e.y_type, at, 1, n, n, vy, v);
+            // the padding of the whole row follows its last ups
+            const int32_t over = n < 8 || j + 8 == g.J ? n + (e.y_pad - 2 * g.J) : n;
+            const int32_t all = over < 8 ? over : 8;
+            store8(e.y, e.y_type, at + g.J, 1, n, all, vy && (g.J & 7) == 0, u);
+            for (int32_t c = 8; c < over; c++) store_elem(e.y, e.y_type, at + g.J + c, 0.0f);
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------------------------------
@@ -222,6 +294,13 @@ __device__ __forceinline__ u32x4 read_free(const char* tile, int row0, int kk, i
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * ROWS * 2));
     const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
     return u32x4{a[0], a[1], b[0], b[1]};
+}
+
+// Orders a wave's own LDS writes before its reads (and the other way round) across lanes.
+__device__ __forceinline__ void wave_lds_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
 // Workgroup -> tile: workgroups go round the 8 XCDs, so each XCD takes a contiguous run of tiles, and a
@@ -316,70 +395,73 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
         cur ^= 1;
     }
 
-    // lane: row i = lane & 15 of a 16x16 block, columns (lane >> 4) * 4 + 0..3
-    const int32_t il = i0 + wi * TI + (lane & 15), jl = (lane >> 4) * 4;
-    if (EPI == kEpiLinear) {
+    // The sums go through LDS, a wave's rows at a time, so that a lane ends with eight neighbours of a row:
+    // results, residuals and gradients move in whole lines, and the epilogue's code stands here once.
+    // Lane: row lane & 15 of a 16 x 16 block, columns (lane >> 4) * 4 + 0..3; 16-byte chunk c of row r is
+    // kept at c ^ r, which spreads both sides over the banks.
+    constexpr int SLAB = FI * TJ * 64 * (THREADS / 64) <= 2 * (A_BYTES + B_BYTES) ? FI : FI / 2;  // blocks of 16 rows
+    static_assert(SLAB * TJ * 64 * (THREADS / 64) <= 2 * (A_BYTES + B_BYTES), "");
+    constexpr int CPR = TJ / 4, CM = CPR < 16 ? CPR - 1 : 15;  // chunks per row
+    constexpr int TJO = PAIRED ? TJ / 2 : TJ, LPR = TJO / 8, RPP = 64 / LPR;  // lanes per row, rows per pass
+    f32x4* slab = reinterpret_cast<f32x4*>(smem) + wave * SLAB * 16 * CPR;
+    const int32_t iw = i0 + wi * TI, jw = j0 + wj * TJO, jl = jw + (lane % LPR) * 8;
+    const bool vy = vec8(g.e.y, g.e.y_type, g.e.y_si, g.e.y_sj), vd = vec8(g.e.dy, g.e.dy_type, g.e.d_si, g.e.d_sj);
+    const bool vr = vec8(g.e.res, g.e.y_type, g.e.r_si, g.e.r_sj);
+    float s0[8], s1[8];
 #pragma unroll
-        for (int i = 0; i < FI; i++)
+    for (int k = 0; k < 8; k++) s0[k] = s1[k] = 0.0f;
+#pragma unroll
+    for (int h = 0; h < FI / SLAB; h++) {
+#pragma unroll
+        for (int i = 0; i < SLAB; i++)
 #pragma unroll
             for (int j = 0; j < FJ; j++) {
-                const int32_t ii = il + i * 16, jj = j0 + wj * TJ + j * 16 + jl;
-                if (g.partial) {
-                    float* o = g.partial + ((int64_t)blockIdx.z * g.I + ii) * g.J + jj;
-                    for (int k = 0; k < 4; k++)
-                        if (ii < g.I && jj + k < g.J) o[k] = acc[i][j][k];
-                } else if (ii < g.I && jj < g.J) {
-                    epi_linear(g.e, acc[i][j], ii, jj, g.J);
+                const int r = i * 16 + (lane & 15), c = j * 4 + (lane >> 4);
+                slab[r * CPR + (c ^ (r & CM))] = acc[h * SLAB + i][j];
+            }
+        wave_lds_sync();
+#pragma unroll 1
+        for (int p = 0; p < SLAB * 16; p += RPP) {
+            const int r = p + lane / LPR, c = (lane % LPR) * 2;
+            const int32_t i = iw + h * SLAB * 16 + r;
+            if (i >= g.I || jl >= g.J) continue;
+            const f32x4 a = slab[r * CPR + (c ^ (r & CM))], b = slab[r * CPR + ((c + 1) ^ (r & CM))];
+            float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+            if (EPI == kEpiLinear && g.partial) {
+                float* o = g.partial + ((int64_t)blockIdx.z * g.I + i) * g.J;
+                store8(o, GS_TYPE_F32, jl, 1, g.J - jl, g.J - jl, (g.J & 3) == 0, v);
+                continue;
+            }
+            float u[8];
+            if (PAIRED) {
+                const int cu = c + CPR / 2;
+                const f32x4 x = slab[r * CPR + (cu ^ (r & CM))], y = slab[r * CPR + ((cu + 1) ^ (r & CM))];
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    u[k] = x[k];
+                    u[4 + k] = y[k];
                 }
             }
-    } else if (EPI == kEpiGated) {
-#pragma unroll
-        for (int i = 0; i < FI; i++)
-#pragma unroll
-            for (int j = 0; j < FJ / 2; j++) {
-                const int32_t ii = il + i * 16, jj = j0 + wj * (TJ / 2) + j * 16 + jl;
-                if (ii < g.I && jj < g.J) epi_gated(g.e, acc[i][j], acc[i][j + FJ / 2], ii, jj, g.J);
-            }
-    } else {
-        constexpr int NJ = EPI == kEpiDGated ? FJ / 2 : FJ;
-        const int64_t strip = (int64_t)ti * WI + wi;
-#pragma unroll
-        for (int j = 0; j < NJ; j++) {
-            const int32_t jj = j0 + wj * (NJ * 16) + j * 16 + jl;
-            f32x4 s0 = {0.0f, 0.0f, 0.0f, 0.0f}, s1 = s0;
-            const int32_t reach = EPI == kEpiDz && g.e.y_pad > g.J ? g.e.y_pad : g.J;
-#pragma unroll
-            for (int i = 0; i < FI; i++) {
-                const int32_t ii = il + i * 16;
-                if (ii < g.I && jj < reach) {
-                    if (EPI == kEpiDz) {
-                        s0 += epi_dz(g.e, acc[i][j], ii, jj, g.J);
-                    } else {
-                        f32x4 dg, du;
-                        epi_dgated(g.e, acc[i][j], acc[i][j + FJ / 2], ii, jj, g.J, dg, du);
-                        s0 += dg;
-                        s1 += du;
-                    }
-                }
-            }
-            if (g.e.colsum) {
-#pragma unroll
-                for (int m = 1; m < 16; m <<= 1)
-#pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        s0[k] += __shfl_xor(s0[k], m);
-                        if (EPI == kEpiDGated) s1[k] += __shfl_xor(s1[k], m);
-                    }
-                if ((lane & 15) == 0) {
-                    const int64_t cols = EPI == kEpiDGated ? 2 * (int64_t)g.J : g.J;
-                    for (int k = 0; k < 4; k++)
-                        if (jj + k < g.J) {
-                            g.e.colsum[strip * cols + jj + k] = s0[k];
-                            if (EPI == kEpiDGated) g.e.colsum[strip * cols + g.J + jj + k] = s1[k];
-                        }
-                }
-            }
+            epi8<EPI>(g, v, u, i, jl, vy, vd, vr, s0, s1);
         }
+        if (h + 1 < FI / SLAB) wave_lds_sync();
+    }
+    if ((EPI == kEpiDz || EPI == kEpiDGated) && g.e.colsum) {
+        const int64_t cols = EPI == kEpiDGated ? 2 * (int64_t)g.J : g.J, strip = (int64_t)ti * WI + wi;
+#pragma unroll
+        for (int m = LPR; m < 64; m <<= 1)
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                s0[k] += __shfl_xor(s0[k], m);
+                if (EPI == kEpiDGated) s1[k] += __shfl_xor(s1[k], m);
+            }
+        if (lane < LPR)
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                if (jl + k < g.J) {
+                    g.e.colsum[strip * cols + jl + k] = s0[k];
+                    if (EPI == kEpiDGated) g.e.colsum[strip * cols + g.J + jl + k] = s1[k];
+                }
     }
 }
 
