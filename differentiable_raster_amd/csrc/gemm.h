@@ -209,14 +209,13 @@ __device__ __forceinline__ void epi8(const GemmArgs& g, float (&v)[8], float (&u
 }
 
 // ---------------------------------------------------------------------------------------------------
-// Loads of a tile: 16-byte chunks through a buffer descriptor whose range ends with the operand, so a
-// chunk outside of it reads zeros.
+// Loads of a tile: 16-byte chunks that go from memory to LDS without passing a register, through a buffer
+// descriptor whose range ends with the operand, so that a chunk outside of it arrives as zeros.  The load
+// puts lane l's chunk at the wave's LDS base + 16 l; the swizzles that keep the later reads free of bank
+// conflicts therefore permute the chunks' sources.
 // ---------------------------------------------------------------------------------------------------
-__device__ __forceinline__ u32x4 buffer_chunk(const void* base, int32_t bytes, int32_t off) {
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00020000);
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
-}
 constexpr int32_t kOutside = 0x7FFFFFF0;  // past every range
+typedef __attribute__((address_space(3))) void lds_void;
 
 // swizzle of a kRowFree tile: the 32-byte granule of k row k, see read_free()
 template <int ROWS>
@@ -231,35 +230,35 @@ struct Operand {
     static_assert(ROWS * 8 % THREADS == 0 && (LAYOUT == kRowK || T::chunk == 8), "");
     static constexpr int ES = 16 / T::chunk;      // bytes of an element
     static constexpr int BK = kStepBytes / ES;    // k per step
+    static constexpr int KPN = LAYOUT == kRowK ? 0 : THREADS / (ROWS / 8);  // k rows between a thread's chunks
     int32_t off[N];   // byte offsets from the step's base
-    int32_t lds[N];   // byte offsets in the tile
-    int32_t first_k[N];
+    int32_t first_k;  // k of the first chunk
 
     __device__ __forceinline__ void init(int tid, int64_t ld, int32_t pair_rows) {
+        static_assert(LAYOUT == kRowK ? THREADS / 8 % 8 == 0 : THREADS % (ROWS / 8) == 0, "");
 #pragma unroll
         for (int n = 0; n < N; n++) {
             const int id = tid + n * THREADS;
-            if (LAYOUT == kRowK) {
-                const int row = id >> 3, c = id & 7;
+            if (LAYOUT == kRowK) {  // THREADS / 8 rows apart: c is the same for every n
+                const int row = id >> 3, c = (id & 7) ^ (row & 7);
                 int64_t src = row;
                 if (PAIRED) {  // rows of a wave's strip: first half gates, second half ups
                     const int w = row / TJ, rr = row % TJ, half = rr / (TJ / 2);
                     src = (int64_t)half * pair_rows + w * (TJ / 2) + rr % (TJ / 2);
                 }
                 off[n] = (int32_t)(src * ld * ES + c * 16);
-                lds[n] = row * 128 + ((c ^ (row & 7)) << 4);
-                first_k[n] = c * T::chunk;
+                if (n == 0) first_k = c * T::chunk;
             } else {
-                const int k = id / (ROWS / 8), c = id % (ROWS / 8);
+                const int k = id / (ROWS / 8), slot = id % (ROWS / 8);
+                const int c = ((slot >> 1) ^ free_swizzle<ROWS>(k)) * 2 + (slot & 1);
                 off[n] = (int32_t)(k * ld * ES + c * 16);
-                lds[n] = k * ROWS * 2 + (((c >> 1) ^ free_swizzle<ROWS>(k)) << 5) + ((c & 1) << 4);
-                first_k[n] = k;
+                if (n == 0) first_k = k;
             }
         }
     }
     // p: first element of the tile's free rows at k = 0; rows: free rows from there to the operand's end
     // (kRowK: at most what the tile reads; kRowFree: columns); left: k from the step's first to the end.
-    __device__ __forceinline__ void load(u32x4 (&r)[N], const char* p, int64_t ld, int64_t k0, int32_t rows, int64_t left) const {
+    __device__ __forceinline__ void load(char* tile, int wave, const char* p, int64_t ld, int64_t k0, int32_t rows, int64_t left) const {
         const bool whole = left >= BK;
         const int32_t l = whole ? BK : (int32_t)left;
         const char* base = LAYOUT == kRowK ? p + k0 * ES : p + k0 * ld * ES;
@@ -267,34 +266,42 @@ struct Operand {
         const int32_t lp = (l + T::chunk - 1) / T::chunk * T::chunk;
         const int32_t bytes = LAYOUT == kRowK ? (int32_t)(((int64_t)(rows - 1) * ld + lp) * ES)
                                               : (int32_t)(((int64_t)(l - 1) * ld + rows) * ES);
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, bytes, 0x00020000);
 #pragma unroll
-        for (int n = 0; n < N; n++) r[n] = buffer_chunk(base, bytes, whole || first_k[n] < l ? off[n] : kOutside);
-    }
-    __device__ __forceinline__ void store(const u32x4 (&r)[N], char* tile) const {
-#pragma unroll
-        for (int n = 0; n < N; n++) *reinterpret_cast<u32x4*>(tile + lds[n]) = r[n];
+        for (int n = 0; n < N; n++)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(tile + n * THREADS * 16 + wave * 1024), 16,
+                                                     whole || first_k + n * KPN < l ? off[n] : kOutside, 0, 0, 0);
     }
 };
 
-// 16 rows from row0 on, chunk step kk (0 or 1) of a kRowK tile: lane (l & 15) its row, (l >> 4) its 8 k.
-__device__ __forceinline__ u32x4 read_k(const char* tile, int row0, int kk, int lane) {
-    const int row = row0 + (lane & 15), c = kk * 4 + (lane >> 4);
-    return *reinterpret_cast<const u32x4*>(tile + row * 128 + ((c ^ (row & 7)) << 4));
-}
-// The same fragment of a kRowFree tile.  One transposing read serves 16 lanes: lane l gives the address of
-// four columns of k row l / 4 and receives column l % 16 of four k rows.  The 32-byte granules of the k rows
-// that one instruction touches are spread over the banks by free_swizzle().
-template <int ROWS>
-__device__ __forceinline__ u32x4 read_free(const char* tile, int row0, int kk, int lane) {
-    const int l = lane & 15, k = kk * 32 + (lane >> 4) * 8 + (l >> 2);
-    const char* p = tile + k * ROWS * 2 + (((row0 >> 4) ^ free_swizzle<ROWS>(k)) << 5) + ((l & 3) << 3);
-    // k and k + 4 (k % 8 < 4) have the same swizzle
-    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * ROWS * 2));
-    const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
-    return u32x4{a[0], a[1], b[0], b[1]};
-}
+// Fragments of a tile for the matrix instruction: lane (l & 15) holds row l of a block of 16, (l >> 4) its 8 k.
+template <int ROWS, int LAYOUT>
+struct Reader {
+    int32_t base;  // byte offset of block 0, first half of the step
+    __device__ __forceinline__ void init(int block0, int lane) {
+        const int l = lane & 15, q = lane >> 4;
+        if (LAYOUT == kRowK) {  // row r keeps its 16-byte chunk c at c ^ (r & 7)
+            base = (block0 * 16 + l) * 128 + ((q ^ (l & 7)) << 4);
+        } else {
+            // One transposing read serves 16 lanes: lane l gives the address of four columns of k row l / 4 and
+            // receives column l % 16 of four k rows.  The 32-byte granules of the k rows that one instruction
+            // touches are spread over the banks by free_swizzle(), the same for k and k + 4 (k % 8 < 4) and for
+            // both halves of a step.
+            const int k = q * 8 + (l >> 2);
+            base = k * ROWS * 2 + ((block0 ^ free_swizzle<ROWS>(k)) << 5) + ((l & 3) << 3);
+        }
+    }
+    // block: multiple blocks from block0, which is a multiple of their number; kk: half of the step
+    __device__ __forceinline__ u32x4 read(const char* tile, int block, int kk) const {
+        if (LAYOUT == kRowK) return *reinterpret_cast<const u32x4*>(tile + (base ^ (kk << 6)) + block * 2048);
+        const char* p = tile + (base ^ (block << 5)) + kk * 32 * ROWS * 2;
+        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * ROWS * 2));
+        const u32x2 a = __builtin_bit_cast(u32x2, lo), b = __builtin_bit_cast(u32x2, hi);
+        return u32x4{a[0], a[1], b[0], b[1]};
+    }
+};
 
 // Orders a wave's own LDS writes before its reads (and the other way round) across lanes.
 __device__ __forceinline__ void wave_lds_sync() {
@@ -317,18 +324,21 @@ __device__ __forceinline__ void tile_of(int32_t id, int32_t ni, int32_t nj, int3
 
 template <class T, int SHAPE, int LA, int LB, int EPI>
 __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(GemmArgs g) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host needs the kernel's name alone
     constexpr int BI = kTileDims[SHAPE].bi, BJ = kTileDims[SHAPE].bj, WI = kTileDims[SHAPE].wi;
     constexpr int THREADS = SHAPE == kTile256 ? 512 : 256, WJ = THREADS / 64 / WI;
     constexpr int TI = BI / WI, TJ = BJ / WJ, FI = TI / 16, FJ = TJ / 16;
     constexpr bool PAIRED = EPI == kEpiGated || EPI == kEpiDGated;
     constexpr int BK = kStepBytes / (16 / T::chunk);
     constexpr int A_BYTES = BI * 128, B_BYTES = BJ * 128;
-    __shared__ __align__(1024) char smem[2 * (A_BYTES + B_BYTES)];
+    // two objects, so that the compiler knows a load into one of them does not touch the other
+    __shared__ __align__(1024) char tile0[A_BYTES + B_BYTES];
+    __shared__ __align__(1024) char tile1[A_BYTES + B_BYTES];
     typedef Operand<T, BI, THREADS, LA, false, TI> OpA;
     typedef Operand<T, BJ, THREADS, LB, PAIRED, TJ> OpB;
     constexpr int ES = OpA::ES;
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wi = wave / WJ, wj = wave % WJ;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wi = wave / WJ, wj = wave % WJ;
     constexpr int BJO = PAIRED ? BJ / 2 : BJ;  // result columns of a tile
     const int32_t ni = (g.I + BI - 1) / BI, nj = (g.J + BJO - 1) / BJO;
     int32_t ti, tj;
@@ -345,9 +355,9 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
     oa.init(tid, g.lda, 0);
     ob.init(tid, g.ldb, g.J);
 
-    const int64_t kt0 = (int64_t)blockIdx.z * g.kt_per_split;
-    const int64_t kt_all = (g.K + BK - 1) / BK;
-    const int64_t kt1 = kt0 + g.kt_per_split < kt_all ? kt0 + g.kt_per_split : kt_all;
+    const int32_t kt0 = (int32_t)blockIdx.z * g.kt_per_split;
+    const int32_t kt_all = (int32_t)((g.K + BK - 1) / BK);
+    const int32_t kt1 = kt0 + g.kt_per_split < kt_all ? kt0 + g.kt_per_split : kt_all;
 
     f32x4 acc[FI][FJ];
 #pragma unroll
@@ -355,55 +365,81 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
 #pragma unroll
         for (int j = 0; j < FJ; j++) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    u32x4 va[OpA::N], vb[OpB::N];
-    if (kt0 < kt1) {
-        oa.load(va, pa, g.lda, kt0 * BK, ra, g.K - kt0 * BK);
-        ob.load(vb, pb, g.ldb, kt0 * BK, rb, g.K - kt0 * BK);
-        oa.store(va, smem);
-        ob.store(vb, smem + A_BYTES);
-    }
-    __syncthreads();
-    int cur = 0;
-    for (int64_t kt = kt0; kt < kt1; kt++) {
-        const bool more = kt + 1 < kt1;
-        if (more) {
-            oa.load(va, pa, g.lda, (kt + 1) * BK, ra, g.K - (kt + 1) * BK);
-            ob.load(vb, pb, g.ldb, (kt + 1) * BK, rb, g.K - (kt + 1) * BK);
-        }
-        const char* ta = smem + cur * (A_BYTES + B_BYTES);
-        const char* tb = ta + A_BYTES;
+    constexpr int H = FI / 2;  // blocks of a in a quarter step
+    Reader<BI, LA> reada;
+    Reader<BJ, LB> readb;
+    reada.init(wi * FI, lane);
+    readb.init(wj * FJ, lane);
+    u32x4 fa[2][H], fb[2][FJ];
+    auto fetch = [&](char* tile, int32_t kt) {
+        const int64_t k = (int64_t)kt * BK;
+        oa.load(tile, wave, pa, g.lda, k, ra, g.K - k);
+        ob.load(tile + A_BYTES, wave, pb, g.ldb, k, rb, g.K - k);
+    };
+    auto read_a = [&](const char* tile, int kk, int half) {
 #pragma unroll
-        for (int kk = 0; kk < 2; kk++) {
-            u32x4 fa[FI], fb[FJ];
+        for (int i = 0; i < H; i++) fa[half][i] = reada.read(tile, half * H + i, kk);
+    };
+    auto read_b = [&](const char* tile, int kk) {
 #pragma unroll
-            for (int i = 0; i < FI; i++)
-                fa[i] = LA == kRowK ? read_k(ta, wi * TI + i * 16, kk, lane) : read_free<BI>(ta, wi * TI + i * 16, kk, lane);
+        for (int j = 0; j < FJ; j++) fb[kk][j] = readb.read(tile + A_BYTES, j, kk);
+    };
+    auto multiply = [&](int kk, int half) {
 #pragma unroll
-            for (int j = 0; j < FJ; j++)
-                fb[j] = LB == kRowK ? read_k(tb, wj * TJ + j * 16, kk, lane) : read_free<BJ>(tb, wj * TJ + j * 16, kk, lane);
+        for (int i = 0; i < H; i++)
 #pragma unroll
-            for (int i = 0; i < FI; i++)
-#pragma unroll
-                for (int j = 0; j < FJ; j++) acc[i][j] = T::mma(fb[j], fa[i], acc[i][j]);
-        }
-        if (more) {
-            char* nt = smem + (cur ^ 1) * (A_BYTES + B_BYTES);
-            oa.store(va, nt);
-            ob.store(vb, nt + A_BYTES);
-        }
+            for (int j = 0; j < FJ; j++) acc[half * H + i][j] = T::mma(fb[kk][j], fa[half][i], acc[half * H + i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // Every load from memory to LDS has landed, and every wave is here.  The barrier alone would not wait for
+    // the loads.
+    auto landed = [&]() {
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
         __syncthreads();
-        cur ^= 1;
+    };
+    // A step works on one tile while the other is filled, in quarters: the fragments of a quarter are read
+    // before the products of the one before it, so that LDS latency hides behind products.  Once every wave
+    // has read its last fragments the tile is free for step kt + 2.
+    auto step = [&](char* tile, char* next, int32_t kt) {
+        read_a(tile, 0, 1);
+        multiply(0, 0);
+        read_a(tile, 1, 0);
+        read_b(tile, 1);
+        multiply(0, 1);
+        read_a(tile, 1, 1);
+        multiply(1, 0);
+        landed();
+        if (kt + 2 < kt1) fetch(tile, kt + 2);
+        if (kt + 1 < kt1) {
+            read_a(next, 0, 0);
+            read_b(next, 0);
+        }
+        multiply(1, 1);
+    };
+    if (kt0 < kt1) fetch(tile0, kt0);
+    if (kt0 + 1 < kt1) fetch(tile1, kt0 + 1);
+    landed();
+    if (kt0 < kt1) {
+        read_a(tile0, 0, 0);
+        read_b(tile0, 0);
     }
+    int32_t kt = kt0;
+    for (; kt + 2 <= kt1; kt += 2) {
+        step(tile0, tile1, kt);
+        step(tile1, tile0, kt + 1);
+    }
+    if (kt < kt1) step(tile0, tile1, kt);
 
     // The sums go through LDS, a wave's rows at a time, so that a lane ends with eight neighbours of a row:
     // results, residuals and gradients move in whole lines, and the epilogue's code stands here once.
     // Lane: row lane & 15 of a 16 x 16 block, columns (lane >> 4) * 4 + 0..3; 16-byte chunk c of row r is
     // kept at c ^ r, which spreads both sides over the banks.
-    constexpr int SLAB = FI * TJ * 64 * (THREADS / 64) <= 2 * (A_BYTES + B_BYTES) ? FI : FI / 2;  // blocks of 16 rows
-    static_assert(SLAB * TJ * 64 * (THREADS / 64) <= 2 * (A_BYTES + B_BYTES), "");
+    constexpr int SLAB = FI * TJ * 64 * (THREADS / 128) <= A_BYTES + B_BYTES ? FI : FI / 2;  // blocks of 16 rows
+    static_assert(SLAB * TJ * 64 * (THREADS / 128) <= A_BYTES + B_BYTES, "");
     constexpr int CPR = TJ / 4, CM = CPR < 16 ? CPR - 1 : 15;  // chunks per row
     constexpr int TJO = PAIRED ? TJ / 2 : TJ, LPR = TJO / 8, RPP = 64 / LPR;  // lanes per row, rows per pass
-    f32x4* slab = reinterpret_cast<f32x4*>(smem) + wave * SLAB * 16 * CPR;
+    constexpr int HALF = THREADS / 128;  // waves whose rows go to the first tile's memory
+    f32x4* slab = reinterpret_cast<f32x4*>(wave < HALF ? tile0 : tile1) + wave % HALF * SLAB * 16 * CPR;
     const int32_t iw = i0 + wi * TI, jw = j0 + wj * TJO, jl = jw + (lane % LPR) * 8;
     const bool vy = vec8(g.e.y, g.e.y_type, g.e.y_si, g.e.y_sj), vd = vec8(g.e.dy, g.e.dy_type, g.e.d_si, g.e.d_sj);
     const bool vr = vec8(g.e.res, g.e.y_type, g.e.r_si, g.e.r_sj);
@@ -463,6 +499,7 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
                     if (EPI == kEpiDGated) g.e.colsum[strip * cols + g.J + jl + k] = s1[k];
                 }
     }
+#endif
 }
 
 template <class T, int SHAPE, int LA, int LB, int EPI>
