@@ -331,9 +331,8 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
     constexpr bool PAIRED = EPI == kEpiGated || EPI == kEpiDGated;
     constexpr int BK = kStepBytes / (16 / T::chunk);
     constexpr int A_BYTES = BI * 128, B_BYTES = BJ * 128;
-    // two objects, so that the compiler knows a load into one of them does not touch the other
-    __shared__ __align__(1024) char tile0[A_BYTES + B_BYTES];
-    __shared__ __align__(1024) char tile1[A_BYTES + B_BYTES];
+    // objects of their own, so that the compiler knows a load into one of them does not touch the others
+    __shared__ __align__(1024) char a0[A_BYTES], a1[A_BYTES], b0[B_BYTES], b1[B_BYTES];
     typedef Operand<T, BI, THREADS, LA, false, TI> OpA;
     typedef Operand<T, BJ, THREADS, LB, PAIRED, TJ> OpB;
     constexpr int ES = OpA::ES;
@@ -371,18 +370,18 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
     reada.init(wi * FI, lane);
     readb.init(wj * FJ, lane);
     u32x4 fa[2][H], fb[2][FJ];
-    auto fetch = [&](char* tile, int32_t kt) {
+    auto fetch = [&](char* ta, char* tb, int32_t kt) {
         const int64_t k = (int64_t)kt * BK;
-        oa.load(tile, wave, pa, g.lda, k, ra, g.K - k);
-        ob.load(tile + A_BYTES, wave, pb, g.ldb, k, rb, g.K - k);
+        oa.load(ta, wave, pa, g.lda, k, ra, g.K - k);
+        ob.load(tb, wave, pb, g.ldb, k, rb, g.K - k);
     };
-    auto read_a = [&](const char* tile, int kk, int half) {
+    auto read_a = [&](const char* ta, int kk, int half) {
 #pragma unroll
-        for (int i = 0; i < H; i++) fa[half][i] = reada.read(tile, half * H + i, kk);
+        for (int i = 0; i < H; i++) fa[half][i] = reada.read(ta, half * H + i, kk);
     };
-    auto read_b = [&](const char* tile, int kk) {
+    auto read_b = [&](const char* tb, int kk) {
 #pragma unroll
-        for (int j = 0; j < FJ; j++) fb[kk][j] = readb.read(tile + A_BYTES, j, kk);
+        for (int j = 0; j < FJ; j++) fb[kk][j] = readb.read(tb, j, kk);
     };
     auto multiply = [&](int kk, int half) {
 #pragma unroll
@@ -400,46 +399,50 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
     // A step works on one tile while the other is filled, in quarters: the fragments of a quarter are read
     // before the products of the one before it, so that LDS latency hides behind products.  Once every wave
     // has read its last fragments the tile is free for step kt + 2.
-    auto step = [&](char* tile, char* next, int32_t kt) {
-        read_a(tile, 0, 1);
+    auto step = [&](char* ta, char* tb, char* next_a, char* next_b, int32_t kt) {
+        read_a(ta, 0, 1);
         multiply(0, 0);
-        read_a(tile, 1, 0);
-        read_b(tile, 1);
+        read_a(ta, 1, 0);
+        read_b(tb, 1);
         multiply(0, 1);
-        read_a(tile, 1, 1);
+        read_a(ta, 1, 1);
         multiply(1, 0);
         landed();
-        if (kt + 2 < kt1) fetch(tile, kt + 2);
+        if (kt + 2 < kt1) fetch(ta, tb, kt + 2);
         if (kt + 1 < kt1) {
-            read_a(next, 0, 0);
-            read_b(next, 0);
+            read_a(next_a, 0, 0);
+            read_b(next_b, 0);
         }
         multiply(1, 1);
     };
-    if (kt0 < kt1) fetch(tile0, kt0);
-    if (kt0 + 1 < kt1) fetch(tile1, kt0 + 1);
+    if (kt0 < kt1) fetch(a0, b0, kt0);
+    if (kt0 + 1 < kt1) fetch(a1, b1, kt0 + 1);
     landed();
     if (kt0 < kt1) {
-        read_a(tile0, 0, 0);
-        read_b(tile0, 0);
+        read_a(a0, 0, 0);
+        read_b(b0, 0);
     }
     int32_t kt = kt0;
     for (; kt + 2 <= kt1; kt += 2) {
-        step(tile0, tile1, kt);
-        step(tile1, tile0, kt + 1);
+        step(a0, b0, a1, b1, kt);
+        step(a1, b1, a0, b0, kt + 1);
     }
-    if (kt < kt1) step(tile0, tile1, kt);
+    if (kt < kt1) step(a0, b0, a1, b1, kt);
 
     // The sums go through LDS, a wave's rows at a time, so that a lane ends with eight neighbours of a row:
     // results, residuals and gradients move in whole lines, and the epilogue's code stands here once.
     // Lane: row lane & 15 of a 16 x 16 block, columns (lane >> 4) * 4 + 0..3; 16-byte chunk c of row r is
     // kept at c ^ r, which spreads both sides over the banks.
-    constexpr int SLAB = FI * TJ * 64 * (THREADS / 128) <= A_BYTES + B_BYTES ? FI : FI / 2;  // blocks of 16 rows
-    static_assert(SLAB * TJ * 64 * (THREADS / 128) <= A_BYTES + B_BYTES, "");
+    constexpr bool BIG_A = A_BYTES > B_BYTES, BIG_B = B_BYTES > A_BYTES;
+    constexpr int PER = BIG_A || BIG_B ? THREADS / 128 : THREADS / 256;  // waves per object: four, or the larger two
+    constexpr int ROOM = (BIG_B ? B_BYTES : A_BYTES) / PER;
+    constexpr int SLAB = FI * TJ * 64 <= ROOM ? FI : FI / 2;  // blocks of 16 rows
+    static_assert(SLAB * TJ * 64 <= ROOM, "");
     constexpr int CPR = TJ / 4, CM = CPR < 16 ? CPR - 1 : 15;  // chunks per row
     constexpr int TJO = PAIRED ? TJ / 2 : TJ, LPR = TJO / 8, RPP = 64 / LPR;  // lanes per row, rows per pass
-    constexpr int HALF = THREADS / 128;  // waves whose rows go to the first tile's memory
-    f32x4* slab = reinterpret_cast<f32x4*>(wave < HALF ? tile0 : tile1) + wave % HALF * SLAB * 16 * CPR;
+    const int object = wave / PER;
+    char* room = BIG_A ? (object ? a1 : a0) : BIG_B ? (object ? b1 : b0) : object == 0 ? a0 : object == 1 ? a1 : object == 2 ? b0 : b1;
+    f32x4* slab = reinterpret_cast<f32x4*>(room + wave % PER * ROOM);
     const int32_t iw = i0 + wi * TI, jw = j0 + wj * TJO, jl = jw + (lane % LPR) * 8;
     const bool vy = vec8(g.e.y, g.e.y_type, g.e.y_si, g.e.y_sj), vd = vec8(g.e.dy, g.e.dy_type, g.e.d_si, g.e.d_sj);
     const bool vr = vec8(g.e.res, g.e.y_type, g.e.r_si, g.e.r_sj);
