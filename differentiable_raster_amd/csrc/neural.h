@@ -63,9 +63,11 @@ hipError_t launch_few_rows_f16(EpiKind kind, bool aligned, const GemmArgs& g, hi
 hipError_t launch_few_rows_e4m3(EpiKind kind, bool aligned, const GemmArgs& g, hipStream_t s);
 
 // dst[r][c] = src[r * s_row + c * s_col] for c < cols, 0 for c in [cols, ld_dst): an operand in the layout the
-// tiled product reads.  src_type / dst_type: gs_type.
+// tiled product reads.  src_type / dst_type: gs_type.  sums (may be null; not for GS_TYPE_E4M3): column sums of
+// the unrounded values per block of rows, [pack_row_blocks(rows)][cols].
+int64_t pack_row_blocks(int64_t rows);
 hipError_t launch_pack(const void* src, int src_type, int64_t s_row, int64_t s_col, int64_t rows, int32_t cols,
-                       void* dst, int dst_type, int64_t ld_dst, hipStream_t s);
+                       void* dst, int dst_type, int64_t ld_dst, float* sums, hipStream_t s);
 // out[c] = sum_r in[r * s_row + c * s_col], in a fixed order.  partial: colsum_partial_floats(rows, cols) floats.
 size_t colsum_partial_floats(int64_t rows, int32_t cols);
 hipError_t launch_colsum(const void* in, int type, int64_t s_row, int64_t s_col, int64_t rows, int32_t cols,

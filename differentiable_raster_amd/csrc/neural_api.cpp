@@ -202,11 +202,11 @@ gs_status forward(const gs_linear_desc* d, bool gated, const void* x, const floa
     const int64_t kp = div_up(o.k, o.chunk) * o.chunk;
     hipError_t e = hipSuccess;
     if (o.pack_x) {
-        e = launch_pack(x, d->type, o.ld_x, 1, o.m, d->in, f.x, d->type, kp, s);
+        e = launch_pack(x, d->type, o.ld_x, 1, o.m, d->in, f.x, d->type, kp, nullptr, s);
         x = f.x, o.ld_x = kp;
     }
     if (e == hipSuccess && o.pack_w) {
-        e = launch_pack(weight, d->type, o.ld_w, 1, o.n, d->in, f.w, d->type, kp, s);
+        e = launch_pack(weight, d->type, o.ld_w, 1, o.n, d->in, f.w, d->type, kp, nullptr, s);
         weight = f.w, o.ld_w = kp;
     }
     if (e != hipSuccess) return launched(e, "operand copy");
@@ -233,7 +233,7 @@ struct BackwardPlan {
     bool need_z;       // dz needs the pre-activation
     int64_t kp, np;    // padded widths of x / weight copies and of dz
     Tiling tz, tx, tw;
-    int64_t strips;    // rows of the column sums' partials out of the z product
+    int64_t strips;    // rows of the column sums' partials out of the z product or the copy of dy
     void *x, *w, *dz, *sums, *sums2, *partial;
     size_t bytes;
 };
@@ -251,12 +251,12 @@ BackwardPlan plan_backward(const gs_linear_desc* d, const Dims& o, bool gated, v
     p.tx = choose(d->type, o.m > 0 ? o.m : 1, o.k, o.n, false, true);
     p.tw = choose(d->type, o.n, o.k, o.m, false, true);
     const TileDims td = kTileDims[p.tz.shape];
-    p.strips = div_up(o.m > 0 ? o.m : 1, td.bi) * td.wi;
+    p.strips = p.need_z ? div_up(o.m > 0 ? o.m : 1, td.bi) * td.wi : pack_row_blocks(o.m);
     if (o.pack_x) p.x = c.take((size_t)o.m * p.kp * es);
     if (o.pack_w) p.w = c.take((size_t)o.n * p.kp * es);
     if (p.need_dz) p.dz = c.take((size_t)o.m * p.np * es);
-    if (p.need_z) p.sums = c.take((size_t)p.strips * o.n * 4);
-    p.sums2 = c.take(colsum_partial_floats(p.need_z ? p.strips : o.m, (int32_t)o.n) * 4);
+    if (p.need_dz) p.sums = c.take((size_t)p.strips * o.n * 4);
+    p.sums2 = c.take(colsum_partial_floats(p.need_dz ? p.strips : o.m, (int32_t)o.n) * 4);
     const size_t px = p.tx.partial_bytes(o.m, o.k), pw = p.tw.partial_bytes(o.n, o.k);
     p.partial = c.take(px > pw ? px : pw);
     p.bytes = c.used;
@@ -281,11 +281,11 @@ gs_status backward(const gs_linear_desc* d, bool gated, const void* x, const voi
     hipError_t e = hipSuccess;
 
     if (o.m > 0 && o.pack_x && (p.need_z || dweight)) {
-        e = launch_pack(x, d->type, o.ld_x, 1, o.m, d->in, p.x, d->type, p.kp, s);
+        e = launch_pack(x, d->type, o.ld_x, 1, o.m, d->in, p.x, d->type, p.kp, nullptr, s);
         if (e != hipSuccess) return launched(e, "operand copy");
     }
     if (o.m > 0 && o.pack_w && (p.need_z || dx)) {
-        e = launch_pack(weight, d->type, o.ld_w, 1, o.n, d->in, p.w, d->type, p.kp, s);
+        e = launch_pack(weight, d->type, o.ld_w, 1, o.n, d->in, p.w, d->type, p.kp, nullptr, s);
         if (e != hipSuccess) return launched(e, "operand copy");
     }
     const void* xo = o.pack_x ? p.x : x;
@@ -306,12 +306,13 @@ gs_status backward(const gs_linear_desc* d, bool gated, const void* x, const voi
         set_tiling(g, p.tz, nullptr);
         e = tiled(d->type, p.tz, kRowK, kRowK, gated ? kEpiDGated : kEpiDz, g, s);
         if (e != hipSuccess) return launched(e, "projection of the backward");
-    } else if (o.m > 0 && p.need_dz && (dx || dweight)) {
-        e = launch_pack(dy, d->y_type, d_si, d_sj, o.m, (int32_t)o.n, p.dz, d->type, p.np, s);
+    } else if (o.m > 0 && p.need_dz) {
+        e = launch_pack(dy, d->y_type, d_si, d_sj, o.m, (int32_t)o.n, p.dz, d->type, p.np,
+                        dbias ? static_cast<float*>(p.sums) : nullptr, s);
         if (e != hipSuccess) return launched(e, "gradient copy");
     }
     if (dbias) {
-        if (p.need_z)
+        if (p.need_dz)
             e = launch_colsum(p.sums, GS_TYPE_F32, o.n, 1, o.m > 0 ? p.strips : 0, (int32_t)o.n, static_cast<float*>(p.sums2), dbias, s);
         else
             e = launch_colsum(dy, d->y_type, d_si, d_sj, o.m, (int32_t)o.n, static_cast<float*>(p.sums2), dbias, s);

@@ -297,20 +297,23 @@ hipError_t bwd_type(const NormArgs& a, int32_t groups, hipStream_t s) {
 
 // ---- operand copies -------------------------------------------------------------------------------
 // A 64 x 64 block through LDS, so that both the rows' and the columns' side move whole lines whichever
-// of the source's axes is contiguous.
+// of the source's axes is contiguous.  sums (optional): the block's column sums, unrounded, [row blocks][cols].
 __global__ __launch_bounds__(256) void pack_kernel(const void* src, int src_type, int64_t s_row, int64_t s_col, int64_t rows,
-                                                   int32_t cols, void* dst, int dst_type, int64_t ld) {
+                                                   int32_t cols, void* dst, int dst_type, int64_t ld, float* sums) {
     __shared__ float tile[64][65];
+    __shared__ float part[4][64];
     const int64_t r0 = (int64_t)blockIdx.x * 64;
     const int32_t c0 = blockIdx.y * 64;
     const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
     if (s_col == 1) {
+#pragma unroll 8
         for (int k = y; k < 64; k += 4) {
             const int64_t r = r0 + k;
             const int32_t c = c0 + x;
             tile[k][x] = r < rows && c < cols ? load_elem(src, src_type, r * s_row + c) : 0.0f;
         }
     } else {
+#pragma unroll 8
         for (int k = y; k < 64; k += 4) {
             const int64_t r = r0 + x;
             const int32_t c = c0 + k;
@@ -318,11 +321,25 @@ __global__ __launch_bounds__(256) void pack_kernel(const void* src, int src_type
         }
     }
     __syncthreads();
-    for (int k = y; k < 64; k += 4) {
-        const int64_t r = r0 + k;
-        const int32_t c = c0 + x;
-        if (r < rows && c < ld) store_elem(dst, dst_type, r * ld + c, tile[k][x]);
+    float s = 0.0f;
+    const int x4 = (threadIdx.x & 15) * 4;  // four columns per thread, 16 rows at a time
+    if ((ld & 3) == 0) {
+        for (int k = threadIdx.x >> 4; k < 64; k += 16) {
+            const int64_t r = r0 + k;
+            if (r < rows && c0 + x4 < ld)
+                store_elem4(dst, dst_type, r * ld + c0 + x4, f32x4{tile[k][x4], tile[k][x4 + 1], tile[k][x4 + 2], tile[k][x4 + 3]});
+        }
+    } else {
+        for (int k = y; k < 64; k += 4) {
+            const int64_t r = r0 + k;
+            if (r < rows && c0 + x < ld) store_elem(dst, dst_type, r * ld + c0 + x, tile[k][x]);
+        }
     }
+    if (!sums) return;
+    for (int k = 0; k < 16; k++) s += tile[y * 16 + k][x];
+    part[y][x] = s;
+    __syncthreads();
+    if (y == 0 && c0 + x < cols) sums[(int64_t)blockIdx.x * cols + c0 + x] = (part[0][x] + part[1][x]) + (part[2][x] + part[3][x]);
 }
 // The same for bytes (8-bit operands), rows contiguous on both sides.
 __global__ __launch_bounds__(256) void pack_bytes_kernel(const uint8_t* src, int64_t s_row, int64_t rows, int32_t cols,
@@ -332,19 +349,33 @@ __global__ __launch_bounds__(256) void pack_bytes_kernel(const uint8_t* src, int
 }
 
 // ---- column sums ----------------------------------------------------------------------------------
-// Stage 1: 64 columns x one part of the rows per workgroup, four rows at a time; the four sums meet in LDS.
-__global__ __launch_bounds__(256) void colsum_kernel(const void* in, int type, int64_t s_row, int64_t s_col, int64_t rows,
-                                                     int32_t cols, int64_t rows_per_part, float* out) {
-    __shared__ float part[4][64];
-    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+// 64 columns x one part of the rows per workgroup: eight lanes of eight columns, 32 rows at a time, and the
+// 32 sums meet in LDS in a fixed order.
+template <class T>
+__global__ __launch_bounds__(256) void colsum_kernel(const void* in, int64_t s_row, int64_t rows, int32_t cols,
+                                                     int64_t rows_per_part, bool vec, float* out) {
+    __shared__ float part[32][65];
+    const int x = (threadIdx.x & 7) * 8, y = threadIdx.x >> 3;
     const int32_t c = blockIdx.x * 64 + x;
     const int64_t r0 = (int64_t)blockIdx.y * rows_per_part, r1 = r0 + rows_per_part < rows ? r0 + rows_per_part : rows;
-    float s = 0.0f;
+    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (c < cols)
-        for (int64_t r = r0 + y; r < r1; r += 4) s += load_elem(in, type, r * s_row + c * s_col);
-    part[y][x] = s;
+#pragma unroll 4
+        for (int64_t r = r0 + y; r < r1; r += 32) {
+            float v[8];
+            load8<T>(in, r * s_row, c, cols, vec, v);
+            for (int k = 0; k < 8; k++) s[k] += v[k];
+        }
+    for (int k = 0; k < 8; k++) part[y][x + k] = s[k];
     __syncthreads();
-    if (y == 0 && c < cols) out[(int64_t)blockIdx.y * cols + c] = (part[0][x] + part[1][x]) + (part[2][x] + part[3][x]);
+    const int n = threadIdx.x & 63, q = threadIdx.x >> 6;
+    float t = 0.0f;
+    for (int k = 0; k < 8; k++) t += part[q * 8 + k][n];
+    __syncthreads();
+    part[q][n] = t;
+    __syncthreads();
+    if (q == 0 && (int32_t)(blockIdx.x * 64) + n < cols)
+        out[(int64_t)blockIdx.y * cols + blockIdx.x * 64 + n] = (part[0][n] + part[1][n]) + (part[2][n] + part[3][n]);
 }
 // Rows along the columns' axis (channel-major input): one part of one column per workgroup.
 __global__ __launch_bounds__(256) void rowsum_kernel(const void* in, int type, int64_t s_col, int64_t rows, int32_t cols,
@@ -358,21 +389,59 @@ __global__ __launch_bounds__(256) void rowsum_kernel(const void* in, int type, i
     if (threadIdx.x == 0) out[(int64_t)blockIdx.y * cols + blockIdx.x] = s;
 }
 
-int64_t colsum_parts(int64_t rows) {
-    int64_t p = (rows + 255) / 256;
-    return p < 1 ? 1 : (p > 512 ? 512 : p);
+// Parts of the rows: 256 rows each at least, about 1024 workgroups at most.
+int64_t colsum_parts(int64_t rows, int32_t cols) {
+    const int64_t strips = (cols + 63) / 64, most = strips >= 512 ? 2 : 1024 / strips;
+    const int64_t p = (rows + 255) / 256;
+    return p < 1 ? 1 : (p > most ? most : p);
+}
+
+hipError_t launch_colsum_stage(const void* in, int type, int64_t s_row, int64_t rows, int32_t cols, int64_t parts, int64_t per,
+                               float* out, hipStream_t s) {
+    const dim3 grid((unsigned)((cols + 63) / 64), (unsigned)parts);
+    const bool vec = (cols & 7) == 0 && (s_row & 7) == 0 && (reinterpret_cast<uintptr_t>(in) & 15) == 0;
+    if (type == GS_TYPE_F32)
+        hipLaunchKernelGGL(colsum_kernel<F32>, grid, dim3(256), 0, s, in, s_row, rows, cols, per, vec, out);
+    else if (type == GS_TYPE_BF16)
+        hipLaunchKernelGGL(colsum_kernel<Bf16>, grid, dim3(256), 0, s, in, s_row, rows, cols, per, vec, out);
+    else
+        hipLaunchKernelGGL(colsum_kernel<F16>, grid, dim3(256), 0, s, in, s_row, rows, cols, per, vec, out);
+    return hipGetLastError();
 }
 
 // ---- join of a split product ----------------------------------------------------------------------
-__global__ __launch_bounds__(256) void reduce_kernel(GemmArgs g) {
+// Four neighbours per group of `lanes` threads, each of which takes every lanes-th part; the parts' order is
+// fixed by the split alone.
+__global__ __launch_bounds__(256) void reduce_kernel(GemmArgs g, int lanes) {
+    __shared__ f32x4 part[256];
+    const int groups = 256 / lanes, x = threadIdx.x % groups, y = threadIdx.x / groups;
     const int64_t per_row = (g.J + 3) / 4, total = per_row * g.I;
-    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < total; n += (int64_t)gridDim.x * 256) {
+    for (int64_t n0 = (int64_t)blockIdx.x * groups; n0 < total; n0 += (int64_t)gridDim.x * groups) {
+        const int64_t n = n0 + x;
         const int32_t i = (int32_t)(n / per_row), j = (int32_t)(n % per_row) * 4;
-        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        const float* p = g.partial + (int64_t)i * g.J + j;
-        for (int s = 0; s < g.splits; s++, p += (int64_t)g.I * g.J)
-            for (int k = 0; k < 4; k++)
-                if (j + k < g.J) v[k] += p[k];
+        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (n < total) {
+            const bool vec = (g.J & 3) == 0;
+            const int64_t step = (int64_t)g.I * g.J;
+            const float* p = g.partial + (int64_t)i * g.J + j + y * step;
+#pragma unroll 4
+            for (int s = y; s < g.splits; s += lanes, p += lanes * step) {
+                if (vec) {
+                    v += *reinterpret_cast<const f32x4*>(p);
+                } else {
+                    for (int k = 0; k < 4; k++)
+                        if (j + k < g.J) v[k] += p[k];
+                }
+            }
+        }
+        if (lanes > 1) {
+            __syncthreads();
+            part[threadIdx.x] = v;
+            __syncthreads();
+            if (y == 0)
+                for (int l = 1; l < lanes; l++) v += part[l * groups + x];
+        }
+        if (y != 0 || n >= total) continue;
         for (int k = 0; k < 4; k++) {
             if (j + k >= g.J) break;
             float z = v[k];
@@ -406,8 +475,10 @@ hipError_t launch_norm_bwd(int type, const NormArgs& a, int32_t groups, hipStrea
     return bwd_type<F32>(a, groups, s);
 }
 
+int64_t pack_row_blocks(int64_t rows) { return (rows + 63) / 64; }
+
 hipError_t launch_pack(const void* src, int src_type, int64_t s_row, int64_t s_col, int64_t rows, int32_t cols, void* dst,
-                       int dst_type, int64_t ld_dst, hipStream_t s) {
+                       int dst_type, int64_t ld_dst, float* sums, hipStream_t s) {
     if (rows <= 0) return hipSuccess;
     if (src_type == GS_TYPE_E4M3) {
         const unsigned blocks = (unsigned)(rows < 65536 ? rows : 65536);
@@ -415,28 +486,36 @@ hipError_t launch_pack(const void* src, int src_type, int64_t s_row, int64_t s_c
                            cols, static_cast<uint8_t*>(dst), ld_dst);
     } else {
         hipLaunchKernelGGL(pack_kernel, dim3((unsigned)((rows + 63) / 64), (unsigned)((ld_dst + 63) / 64)), dim3(256), 0, s,
-                           src, src_type, s_row, s_col, rows, cols, dst, dst_type, ld_dst);
+                           src, src_type, s_row, s_col, rows, cols, dst, dst_type, ld_dst, sums);
     }
     return hipGetLastError();
 }
 
-size_t colsum_partial_floats(int64_t rows, int32_t cols) { return (size_t)colsum_parts(rows) * cols; }
+size_t colsum_partial_floats(int64_t rows, int32_t cols) {
+    const int64_t parts = colsum_parts(rows, cols);
+    return (size_t)(parts + colsum_parts(parts, cols)) * cols;
+}
 
 hipError_t launch_colsum(const void* in, int type, int64_t s_row, int64_t s_col, int64_t rows, int32_t cols, float* partial,
                          float* out, hipStream_t s) {
-    const int64_t parts = colsum_parts(rows), per = rows > 0 ? (rows + parts - 1) / parts : 1;
-    float* first = parts > 1 ? partial : out;
-    if (s_row == 1 && s_col != 1)
+    int64_t parts = colsum_parts(rows, cols), per = rows > 0 ? (rows + parts - 1) / parts : 1;
+    float* to = parts > 1 ? partial : out;
+    hipError_t e;
+    if (s_row == 1 && s_col != 1) {
         hipLaunchKernelGGL(rowsum_kernel, dim3((unsigned)cols, (unsigned)parts), dim3(256), 0, s, in, type, s_col, rows, cols,
-                           per, first);
-    else
-        hipLaunchKernelGGL(colsum_kernel, dim3((unsigned)((cols + 63) / 64), (unsigned)parts), dim3(256), 0, s, in, type,
-                           s_row, s_col, rows, cols, per, first);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || parts == 1) return e;
-    hipLaunchKernelGGL(colsum_kernel, dim3((unsigned)((cols + 63) / 64), 1), dim3(256), 0, s, partial, GS_TYPE_F32, (int64_t)cols,
-                       (int64_t)1, parts, cols, parts, out);
-    return hipGetLastError();
+                           per, to);
+        e = hipGetLastError();
+    } else {
+        e = launch_colsum_stage(in, type, s_row, rows, cols, parts, per, to, s);
+    }
+    while (e == hipSuccess && parts > 1) {
+        const int64_t next = colsum_parts(parts, cols);
+        float* dst = next > 1 ? partial + parts * cols : out;
+        e = launch_colsum_stage(to, GS_TYPE_F32, cols, parts, cols, next, (parts + next - 1) / next, dst, s);
+        to = dst;
+        parts = next;
+    }
+    return e;
 }
 
 hipError_t launch_gemm(int type, TileShape shape, Layout la, Layout lb, EpiKind kind, const GemmArgs& g, hipStream_t s) {
@@ -452,10 +531,11 @@ hipError_t launch_few_rows(int type, EpiKind kind, bool aligned, const GemmArgs&
 }
 
 hipError_t launch_gemm_reduce(const GemmArgs& g, hipStream_t s) {
+    const int lanes = g.splits >= 32 ? 16 : g.splits >= 8 ? 4 : 1;
     const int64_t total = ((int64_t)g.J + 3) / 4 * g.I;
-    int64_t blocks = (total + 255) / 256;
+    int64_t blocks = (total + 256 / lanes - 1) / (256 / lanes);
     if (blocks > 8192) blocks = 8192;
-    hipLaunchKernelGGL(reduce_kernel, dim3((unsigned)blocks), dim3(256), 0, s, g);
+    hipLaunchKernelGGL(reduce_kernel, dim3((unsigned)blocks), dim3(256), 0, s, g, lanes);
     return hipGetLastError();
 }
 
