@@ -12,6 +12,8 @@
 // operand), so a lane stores four neighbours of a row at once.
 #pragma once
 
+#include <type_traits>
+
 #include "elem.h"
 #include "neural.h"
 
@@ -148,10 +150,11 @@ __device__ __forceinline__ void pre8(const Epi& e, float (&v)[8], int32_t i, int
     }
 }
 
-// v: the sums of row i, columns j.. (of the gates); u: of the ups.  s0, s1 collect the column sums.
+// v: the sums of row i, columns j.. (of the gates); u: of the ups; d: residual or gradient of the result there.
+// s0, s1 collect the column sums.
 template <int EPI>
-__device__ __forceinline__ void epi8(const GemmArgs& g, float (&v)[8], float (&u)[8], int32_t i, int32_t j, bool vy, bool vd, bool vr,
-                                     float (&s0)[8], float (&s1)[8]) {
+__device__ __forceinline__ void epi8(const GemmArgs& g, float (&v)[8], float (&u)[8], const float (&d)[8], int32_t i, int32_t j,
+                                     bool vy, float (&s0)[8], float (&s1)[8]) {
     const Epi& e = g.e;
     const int32_t n = g.J - j < 8 ? g.J - j : 8;
     const int64_t at = (int64_t)i * e.y_si + (int64_t)j * e.y_sj;
@@ -163,10 +166,8 @@ __device__ __forceinline__ void epi8(const GemmArgs& g, float (&v)[8], float (&u
             for (int k = 0; k < 8; k++) v[k] = act_value(v[k], e.act);
         }
         if (e.res) {
-            float r[8];
-            load8(e.res, e.y_type, (int64_t)i * e.r_si + (int64_t)j * e.r_sj, e.r_sj, n, vr, r);
 #pragma unroll
-            for (int k = 0; k < 8; k++) v[k] += r[k];
+            for (int k = 0; k < 8; k++) v[k] += d[k];
         }
         store8(e.y, e.y_type, at, e.y_sj, n, end, vy, v);
     } else if (EPI == kEpiGated) {
@@ -175,8 +176,6 @@ __device__ __forceinline__ void epi8(const GemmArgs& g, float (&v)[8], float (&u
         for (int k = 0; k < 8; k++) v[k] = act_value(v[k], e.act) * u[k];
         store8(e.y, e.y_type, at, e.y_sj, n, n, vy, v);
     } else {
-        float d[8];
-        load8(e.dy, e.dy_type, (int64_t)i * e.d_si + (int64_t)j * e.d_sj, e.d_sj, n, vd, d);
         if (EPI == kEpiDz) {  // dz = dy act'(z)
 #pragma unroll
             for (int k = 0; k < 8; k++) {
@@ -291,6 +290,10 @@ struct Reader {
             base = k * ROWS * 2 + ((block0 ^ free_swizzle<ROWS>(k)) << 5) + ((l & 3) << 3);
         }
     }
+    // Keeps the compiler from holding an address per block in registers over the whole loop, which the sums need.
+    __device__ __forceinline__ void renew() {
+        if (LAYOUT == kRowFree) asm volatile("" : "+v"(base));
+    }
     // block: multiple blocks from block0, which is a multiple of their number; kk: half of the step
     __device__ __forceinline__ u32x4 read(const char* tile, int block, int kk) const {
         if (LAYOUT == kRowK) return *reinterpret_cast<const u32x4*>(tile + (base ^ (kk << 6)) + block * 2048);
@@ -400,6 +403,8 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
     // before the products of the one before it, so that LDS latency hides behind products.  Once every wave
     // has read its last fragments the tile is free for step kt + 2.
     auto step = [&](char* ta, char* tb, char* next_a, char* next_b, int32_t kt) {
+        reada.renew();
+        readb.renew();
         read_a(ta, 0, 1);
         multiply(0, 0);
         read_a(ta, 1, 0);
@@ -409,19 +414,15 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
         multiply(1, 0);
         landed();
         if (kt + 2 < kt1) fetch(ta, tb, kt + 2);
-        if (kt + 1 < kt1) {
-            read_a(next_a, 0, 0);
-            read_b(next_b, 0);
-        }
+        read_a(next_a, 0, 0);  // after the last step: values that no product takes
+        read_b(next_b, 0);
         multiply(1, 1);
     };
     if (kt0 < kt1) fetch(a0, b0, kt0);
     if (kt0 + 1 < kt1) fetch(a1, b1, kt0 + 1);
     landed();
-    if (kt0 < kt1) {
-        read_a(a0, 0, 0);
-        read_b(b0, 0);
-    }
+    read_a(a0, 0, 0);
+    read_b(b0, 0);
     int32_t kt = kt0;
     for (; kt + 2 <= kt1; kt += 2) {
         step(a0, b0, a1, b1, kt);
@@ -449,8 +450,8 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
     float s0[8], s1[8];
 #pragma unroll
     for (int k = 0; k < 8; k++) s0[k] = s1[k] = 0.0f;
-#pragma unroll
-    for (int h = 0; h < FI / SLAB; h++) {
+    auto slab_rows = [&](auto part) {
+        constexpr int h = decltype(part)::value;
 #pragma unroll
         for (int i = 0; i < SLAB; i++)
 #pragma unroll
@@ -459,31 +460,53 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
                 slab[r * CPR + (c ^ (r & CM))] = acc[h * SLAB + i][j];
             }
         wave_lds_sync();
+        constexpr int PASSES = SLAB * 16 / RPP, AHEAD = PASSES < 4 ? PASSES : 4;
 #pragma unroll 1
-        for (int p = 0; p < SLAB * 16; p += RPP) {
-            const int r = p + lane / LPR, c = (lane % LPR) * 2;
-            const int32_t i = iw + h * SLAB * 16 + r;
-            if (i >= g.I || jl >= g.J) continue;
-            const f32x4 a = slab[r * CPR + (c ^ (r & CM))], b = slab[r * CPR + ((c + 1) ^ (r & CM))];
-            float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-            if (EPI == kEpiLinear && g.partial) {
-                float* o = g.partial + ((int64_t)blockIdx.z * g.I + i) * g.J;
-                store8(o, GS_TYPE_F32, jl, 1, g.J - jl, g.J - jl, (g.J & 3) == 0, v);
-                continue;
-            }
-            float u[8];
-            if (PAIRED) {
-                const int cu = c + CPR / 2;
-                const f32x4 x = slab[r * CPR + (cu ^ (r & CM))], y = slab[r * CPR + ((cu + 1) ^ (r & CM))];
+        for (int p0 = 0; p0 < PASSES; p0 += AHEAD) {
+            const int ib = iw + h * SLAB * 16 + p0 * RPP + lane / LPR;
+            const int32_t n = g.J - jl < 8 ? g.J - jl : 8;
+            float d[AHEAD][8];  // what several passes read from memory, in flight together
+            if (EPI == kEpiLinear ? g.e.res != nullptr : EPI != kEpiGated) {
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    u[k] = x[k];
-                    u[4 + k] = y[k];
+                for (int p = 0; p < AHEAD; p++) {
+                    const int32_t i = ib + p * RPP;
+                    const int32_t m = i < g.I ? n : 0;
+                    if (EPI == kEpiLinear)
+                        load8(g.e.res, g.e.y_type, (int64_t)i * g.e.r_si + (int64_t)jl * g.e.r_sj, g.e.r_sj, m, vr, d[p]);
+                    else
+                        load8(g.e.dy, g.e.dy_type, (int64_t)i * g.e.d_si + (int64_t)jl * g.e.d_sj, g.e.d_sj, m, vd, d[p]);
                 }
             }
-            epi8<EPI>(g, v, u, i, jl, vy, vd, vr, s0, s1);
+#pragma unroll
+            for (int p = 0; p < AHEAD; p++) {
+                const int r = (p0 + p) * RPP + lane / LPR, c = (lane % LPR) * 2;
+                const int32_t i = ib + p * RPP;
+                if (i >= g.I || jl >= g.J) continue;
+                const f32x4 a = slab[r * CPR + (c ^ (r & CM))], b = slab[r * CPR + ((c + 1) ^ (r & CM))];
+                float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+                if (EPI == kEpiLinear && g.partial) {
+                    float* o = g.partial + ((int64_t)blockIdx.z * g.I + i) * g.J;
+                    store8(o, GS_TYPE_F32, jl, 1, g.J - jl, g.J - jl, (g.J & 3) == 0, v);
+                    continue;
+                }
+                float u[8];
+                if (PAIRED) {
+                    const int cu = c + CPR / 2;
+                    const f32x4 x = slab[r * CPR + (cu ^ (r & CM))], y = slab[r * CPR + ((cu + 1) ^ (r & CM))];
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        u[k] = x[k];
+                        u[4 + k] = y[k];
+                    }
+                }
+                epi8<EPI>(g, v, u, d[p], i, jl, vy, s0, s1);
+            }
         }
-        if (h + 1 < FI / SLAB) wave_lds_sync();
+    };
+    slab_rows(std::integral_constant<int, 0>());
+    if constexpr (FI / SLAB > 1) {
+        wave_lds_sync();
+        slab_rows(std::integral_constant<int, 1>());
     }
     if ((EPI == kEpiDz || EPI == kEpiDGated) && g.e.colsum) {
         const int64_t cols = EPI == kEpiDGated ? 2 * (int64_t)g.J : g.J, strip = (int64_t)ti * WI + wi;

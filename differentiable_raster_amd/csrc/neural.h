@@ -68,10 +68,10 @@ hipError_t launch_few_rows_e4m3(EpiKind kind, bool aligned, const GemmArgs& g, h
 int64_t pack_row_blocks(int64_t rows);
 hipError_t launch_pack(const void* src, int src_type, int64_t s_row, int64_t s_col, int64_t rows, int32_t cols,
                        void* dst, int dst_type, int64_t ld_dst, float* sums, hipStream_t s);
-// out[c] = sum_r in[r * s_row + c * s_col], in a fixed order.  partial: colsum_partial_floats(rows, cols) floats.
+// out[c] = sum_r in[r * s_row + c], in a fixed order.  partial: colsum_partial_floats(rows, cols) floats.
 size_t colsum_partial_floats(int64_t rows, int32_t cols);
-hipError_t launch_colsum(const void* in, int type, int64_t s_row, int64_t s_col, int64_t rows, int32_t cols,
-                         float* partial, float* out, hipStream_t s);
+hipError_t launch_colsum(const void* in, int type, int64_t s_row, int64_t rows, int32_t cols, float* partial, float* out,
+                         hipStream_t s);
 
 struct NormArgs {
     int64_t rows;

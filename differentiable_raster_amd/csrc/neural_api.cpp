@@ -313,9 +313,9 @@ gs_status backward(const gs_linear_desc* d, bool gated, const void* x, const voi
     }
     if (dbias) {
         if (p.need_dz)
-            e = launch_colsum(p.sums, GS_TYPE_F32, o.n, 1, o.m > 0 ? p.strips : 0, (int32_t)o.n, static_cast<float*>(p.sums2), dbias, s);
+            e = launch_colsum(p.sums, GS_TYPE_F32, o.n, o.m > 0 ? p.strips : 0, (int32_t)o.n, static_cast<float*>(p.sums2), dbias, s);
         else
-            e = launch_colsum(dy, d->y_type, d_si, d_sj, o.m, (int32_t)o.n, static_cast<float*>(p.sums2), dbias, s);
+            e = launch_colsum(dy, d->y_type, o.ld_y, o.m, (int32_t)o.n, static_cast<float*>(p.sums2), dbias, s);
         if (e != hipSuccess) return launched(e, "bias gradient");
     }
     const void* dz = p.need_dz ? p.dz : dy;
@@ -446,7 +446,7 @@ gs_status gs_rmsnorm_bwd(const gs_norm_desc* d, const void* s, const float* weig
         if (st != GS_OK) return st;
     }
     if (!dweight) return GS_OK;
-    return launched(launch_colsum(partial, GS_TYPE_F32, d->width, 1, groups, d->width, partial2, dweight, hs), "weight gradient");
+    return launched(launch_colsum(partial, GS_TYPE_F32, d->width, groups, d->width, partial2, dweight, hs), "weight gradient");
 }
 
 size_t gs_linear_workspace_size(const gs_linear_desc* d) { return forward_ws(d, false); }

@@ -377,18 +377,6 @@ __global__ __launch_bounds__(256) void colsum_kernel(const void* in, int64_t s_r
     if (q == 0 && (int32_t)(blockIdx.x * 64) + n < cols)
         out[(int64_t)blockIdx.y * cols + blockIdx.x * 64 + n] = (part[0][n] + part[1][n]) + (part[2][n] + part[3][n]);
 }
-// Rows along the columns' axis (channel-major input): one part of one column per workgroup.
-__global__ __launch_bounds__(256) void rowsum_kernel(const void* in, int type, int64_t s_col, int64_t rows, int32_t cols,
-                                                     int64_t rows_per_part, float* out) {
-    __shared__ float lds[16];
-    const int64_t r0 = (int64_t)blockIdx.y * rows_per_part, r1 = r0 + rows_per_part < rows ? r0 + rows_per_part : rows;
-    const int64_t base = (int64_t)blockIdx.x * s_col;
-    float s = 0.0f;
-    for (int64_t r = r0 + threadIdx.x; r < r1; r += 256) s += load_elem(in, type, base + r);
-    s = row_sum<256>(s, lds);
-    if (threadIdx.x == 0) out[(int64_t)blockIdx.y * cols + blockIdx.x] = s;
-}
-
 // Parts of the rows: 256 rows each at least, about 1024 workgroups at most.
 int64_t colsum_parts(int64_t rows, int32_t cols) {
     const int64_t strips = (cols + 63) / 64, most = strips >= 512 ? 2 : 1024 / strips;
@@ -496,18 +484,12 @@ size_t colsum_partial_floats(int64_t rows, int32_t cols) {
     return (size_t)(parts + colsum_parts(parts, cols)) * cols;
 }
 
-hipError_t launch_colsum(const void* in, int type, int64_t s_row, int64_t s_col, int64_t rows, int32_t cols, float* partial,
-                         float* out, hipStream_t s) {
-    int64_t parts = colsum_parts(rows, cols), per = rows > 0 ? (rows + parts - 1) / parts : 1;
+hipError_t launch_colsum(const void* in, int type, int64_t s_row, int64_t rows, int32_t cols, float* partial, float* out,
+                         hipStream_t s) {
+    int64_t parts = colsum_parts(rows, cols);
+    const int64_t per = rows > 0 ? (rows + parts - 1) / parts : 1;
     float* to = parts > 1 ? partial : out;
-    hipError_t e;
-    if (s_row == 1 && s_col != 1) {
-        hipLaunchKernelGGL(rowsum_kernel, dim3((unsigned)cols, (unsigned)parts), dim3(256), 0, s, in, type, s_col, rows, cols,
-                           per, to);
-        e = hipGetLastError();
-    } else {
-        e = launch_colsum_stage(in, type, s_row, rows, cols, parts, per, to, s);
-    }
+    hipError_t e = launch_colsum_stage(in, type, s_row, rows, cols, parts, per, to, s);
     while (e == hipSuccess && parts > 1) {
         const int64_t next = colsum_parts(parts, cols);
         float* dst = next > 1 ? partial + parts * cols : out;
