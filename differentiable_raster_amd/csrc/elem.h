@@ -96,4 +96,39 @@ __device__ __forceinline__ void act_both(float z, int act, float& v, float& d) {
     }
 }
 
+// Eight values at once: the choice of the activation is made once.
+template <int ACT>
+__device__ __forceinline__ void act8_of(float (&v)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; k++) v[k] = act_value(v[k], ACT);
+}
+__device__ __forceinline__ void act8(float (&v)[8], int act) {
+    if (act == GS_ACT_SILU)
+        act8_of<GS_ACT_SILU>(v);
+    else if (act == GS_ACT_GELU)
+        act8_of<GS_ACT_GELU>(v);
+    else if (act == GS_ACT_RELU)
+        act8_of<GS_ACT_RELU>(v);
+}
+// v becomes the activation's value, d its derivative.
+template <int ACT>
+__device__ __forceinline__ void act8_both_of(float (&v)[8], float (&d)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+        float a;
+        act_both(v[k], ACT, a, d[k]);
+        v[k] = a;
+    }
+}
+__device__ __forceinline__ void act8_both(float (&v)[8], float (&d)[8], int act) {
+    if (act == GS_ACT_SILU)
+        act8_both_of<GS_ACT_SILU>(v, d);
+    else if (act == GS_ACT_GELU)
+        act8_both_of<GS_ACT_GELU>(v, d);
+    else if (act == GS_ACT_RELU)
+        act8_both_of<GS_ACT_RELU>(v, d);
+    else
+        act8_both_of<GS_ACT_NONE>(v, d);
+}
+
 }  // namespace gsmi

@@ -136,63 +136,73 @@ __device__ __forceinline__ void store8(void* p, int type, int64_t at, int64_t sj
             if (k < end) store_elem(p, type, at + k * sj, k < n ? v[k] : 0.0f);
     }
 }
-// scale and bias; shift: the columns' offset in scale_j and bias (the ups have J)
-__device__ __forceinline__ void pre8(const Epi& e, float (&v)[8], int32_t i, int32_t j, int32_t n, int32_t shift) {
-    if (e.scale_i) {
-        const float si = e.scale_i[i];
+// What the epilogue needs of a lane's eight columns, the same for every row: bias and scale; shift: the
+// columns' offset in both (the ups have J).
+struct Columns {
+    float bias[8], scale[8];
+    __device__ __forceinline__ void load(const Epi& e, int32_t j, int32_t J, int32_t shift) {
 #pragma unroll
-        for (int k = 0; k < 8; k++) v[k] *= k < n ? si * e.scale_j[shift + j + k] : 0.0f;
+        for (int k = 0; k < 8; k++) {
+            const bool in = j + k < J;
+            bias[k] = e.bias && !e.bias_on_i && in ? e.bias[shift + j + k] : 0.0f;
+            scale[k] = e.scale_j && in ? e.scale_j[shift + j + k] : 1.0f;
+        }
     }
-    if (e.bias) {
-        const float bi = e.bias_on_i ? e.bias[i] : 0.0f;
+    __device__ __forceinline__ void apply(const Epi& e, float (&v)[8], int32_t i) const {
+        if (e.scale_i) {
+            const float si = e.scale_i[i];
 #pragma unroll
-        for (int k = 0; k < 8; k++) v[k] += e.bias_on_i ? bi : (k < n ? e.bias[shift + j + k] : 0.0f);
+            for (int k = 0; k < 8; k++) v[k] *= si * scale[k];
+        }
+        if (e.bias) {
+            const float bi = e.bias_on_i ? e.bias[i] : 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; k++) v[k] += bias[k] + bi;
+        }
     }
-}
+};
 
 // v: the sums of row i, columns j.. (of the gates); u: of the ups; d: residual or gradient of the result there.
 // s0, s1 collect the column sums.
 template <int EPI>
-__device__ __forceinline__ void epi8(const GemmArgs& g, float (&v)[8], float (&u)[8], const float (&d)[8], int32_t i, int32_t j,
-                                     bool vy, float (&s0)[8], float (&s1)[8]) {
+__device__ __forceinline__ void epi8(const GemmArgs& g, float (&v)[8], float (&u)[8], const float (&d)[8], const Columns& cv,
+                                     const Columns& cu, int32_t i, int32_t j, bool vy, float (&s0)[8], float (&s1)[8]) {
     const Epi& e = g.e;
     const int32_t n = g.J - j < 8 ? g.J - j : 8;
     const int64_t at = (int64_t)i * e.y_si + (int64_t)j * e.y_sj;
     const int32_t end = e.y_pad > g.J ? (e.y_pad - j < 8 ? e.y_pad - j : 8) : n;
-    pre8(e, v, i, j, n, 0);
+    cv.apply(e, v, i);
     if (EPI == kEpiLinear) {
-        if (e.act != GS_ACT_NONE) {
-#pragma unroll
-            for (int k = 0; k < 8; k++) v[k] = act_value(v[k], e.act);
-        }
+        act8(v, e.act);
         if (e.res) {
 #pragma unroll
             for (int k = 0; k < 8; k++) v[k] += d[k];
         }
         store8(e.y, e.y_type, at, e.y_sj, n, end, vy, v);
     } else if (EPI == kEpiGated) {
-        pre8(e, u, i, j, n, g.J);
+        cu.apply(e, u, i);
+        act8(v, e.act);
 #pragma unroll
-        for (int k = 0; k < 8; k++) v[k] = act_value(v[k], e.act) * u[k];
+        for (int k = 0; k < 8; k++) v[k] *= u[k];
         store8(e.y, e.y_type, at, e.y_sj, n, n, vy, v);
     } else {
         if (EPI == kEpiDz) {  // dz = dy act'(z)
+            float da[8];
+            act8_both(v, da, e.act);
 #pragma unroll
             for (int k = 0; k < 8; k++) {
-                float a, da;
-                act_both(v[k], e.act, a, da);
-                v[k] = k < n ? d[k] * da : 0.0f;
+                v[k] = k < n ? d[k] * da[k] : 0.0f;
                 s0[k] += v[k];
             }
             store8(e.y, e.y_type, at, e.y_sj, n, end, vy, v);
         } else {  // dgate = dh up act'(gate) at column j, dup = dh act(gate) at column J + j
-            pre8(e, u, i, j, n, g.J);
+            cu.apply(e, u, i);
+            float da[8];
+            act8_both(v, da, e.act);
 #pragma unroll
             for (int k = 0; k < 8; k++) {
-                float a, da;
-                act_both(v[k], e.act, a, da);
-                const float up = u[k];
-                v[k] = k < n ? d[k] * up * da : 0.0f;
+                const float a = v[k];
+                v[k] = k < n ? d[k] * u[k] * da[k] : 0.0f;
                 u[k] = k < n ? d[k] * a : 0.0f;
                 s0[k] += v[k];
                 s1[k] += u[k];
@@ -447,6 +457,9 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
     const int32_t iw = i0 + wi * TI, jw = j0 + wj * TJO, jl = jw + (lane % LPR) * 8;
     const bool vy = vec8(g.e.y, g.e.y_type, g.e.y_si, g.e.y_sj), vd = vec8(g.e.dy, g.e.dy_type, g.e.d_si, g.e.d_sj);
     const bool vr = vec8(g.e.res, g.e.y_type, g.e.r_si, g.e.r_sj);
+    Columns cv, cu;
+    cv.load(g.e, jl, g.J, 0);
+    if (PAIRED) cu.load(g.e, jl, g.J, g.J);
     float s0[8], s1[8];
 #pragma unroll
     for (int k = 0; k < 8; k++) s0[k] = s1[k] = 0.0f;
@@ -499,7 +512,7 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
                         u[4 + k] = y[k];
                     }
                 }
-                epi8<EPI>(g, v, u, d[p], i, jl, vy, s0, s1);
+                epi8<EPI>(g, v, u, d[p], cv, cu, i, jl, vy, s0, s1);
             }
         }
     };

@@ -48,19 +48,27 @@ int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 Tiling choose(int type, int64_t I, int64_t J, int64_t K, bool paired, bool may_split) {
     const int64_t bk = kStepBytes / elem_bytes(type), kt = div_up(K, bk) > 0 ? div_up(K, bk) : 1;
     const int64_t cols = paired ? 2 * J : J;
-    // steps that a CU takes per microsecond of a 256 x 256 tile's step, by shape
-    static const double eff[kTileShapes] = {1.0, 0.8, 0.5, 0.65, 0.65};
+    // A step's cost in us when a CU is full of such tiles, the least time between two steps of one tile (the
+    // latency of its loads), and how many of them a CU holds; measured over products of 59 x 64 x 300001 to
+    // 8192 x 8192 x 8192.  Small tiles win wherever tiles are few or steps are: 512 x 1024 x 1024 takes 8 us in
+    // tiles of 64 and 16 in tiles of 128; 8192 x 1024 x 4096 takes 71 in tiles of 128 and 94 in tiles of 64.
+    static const double full[kTileShapes] = {1.8, 0.55, 0.19, 0.62, 0.62};
+    static const double least[kTileShapes] = {1.9, 0.85, 0.50, 0.85, 0.85};
+    static const int held[kTileShapes] = {1, 2, 5, 2, 2};
     Tiling best{kTile64, 1, (int32_t)kt};
     double best_t = 1e300;
     for (int s = 0; s < kTileShapes; s++) {
         const TileDims d = kTileDims[s];
         const int64_t tiles = div_up(I, d.bi) * div_up(cols, d.bj);
-        const double step = 0.7 * (double)(d.bi * d.bj) / 65536.0 / eff[s];  // us per step
-        for (int64_t splits = 1; splits <= (may_split ? 64 : 1); splits *= 2) {
-            if (splits > 1 && kt / splits < 4) break;
-            const int64_t per = div_up(kt, splits);
-            double t = (double)div_up(tiles * splits, 256) * ((double)per * step + 2.0);
-            if (splits > 1) t += 3.0 + (double)splits * I * J * 8.0 / 3e6;  // the raw sums, written and read
+        // a tile's own start and end: its first loads and its epilogue, whose bytes grow with its area
+        const double ends = 1.5 + d.bi * d.bj / 8192.0;
+        for (int64_t splits = 1; splits <= (may_split ? 2048 : 1); splits *= 2) {
+            if (splits > 1 && (kt / splits < 4 || splits * I * J > (int64_t(1) << 26))) break;
+            const int64_t per = div_up(kt, splits), each = div_up(tiles * splits, 256);
+            const int64_t rounds = div_up(each, held[s]), busy = each < held[s] ? each : held[s];
+            const double step = full[s] * busy > least[s] ? full[s] * busy : least[s];
+            double t = (double)per * step * (rounds - 1 + (each - (rounds - 1) * held[s]) / (double)busy) + ends * rounds;
+            if (splits > 1) t += 4.0 + (double)splits * I * J * 8.0 / 3e6;  // the raw sums, written and read
             if (t < best_t * 0.999) {
                 best_t = t;
                 best = Tiling{(TileShape)s, (int32_t)div_up(kt, per), (int32_t)per};
