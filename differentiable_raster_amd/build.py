@@ -13,7 +13,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgsmi.so")
 SOURCES = ["project.hip", "project_bwd.hip", "scan.hip", "sort.hip", "bin.hip", "raster.hip", "sparse.hip",
            "compose.hip", "adam.hip", "check.hip", "api.cpp", "gemm_bf16.hip", "gemm_f16.hip", "gemm_e4m3.hip",
-           "rows.hip", "neural_api.cpp"]
+           "narrow.hip", "rows.hip", "neural_api.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

@@ -62,6 +62,29 @@ hipError_t launch_few_rows_bf16(EpiKind kind, bool aligned, const GemmArgs& g, h
 hipError_t launch_few_rows_f16(EpiKind kind, bool aligned, const GemmArgs& g, hipStream_t s);
 hipError_t launch_few_rows_e4m3(EpiKind kind, bool aligned, const GemmArgs& g, hipStream_t s);
 
+// The backward of a narrow map over many rows in one pass (narrow.hip).
+struct NarrowArgs {
+    const void *x, *w;      // 16-byte aligned rows, k a multiple of 8
+    int64_t ldx, ldw;
+    int32_t rows, k, n;     // n: weight rows (gated: gates, then ups)
+    const float* bias;
+    int32_t act;
+    const void* dy;
+    int64_t d_si, d_sj;
+    int32_t dy_type;
+    void* dx;               // optional
+    int64_t ld_dx;
+    int32_t dx_vec;         // dx takes 8-byte stores
+    float* dw_partial;      // optional: [groups][n][k]
+    float* db_partial;      // optional: [db_rows][n]
+};
+struct NarrowShape {
+    int kp, np;             // padded k and n; kp == 0: not served
+    int groups, db_rows;    // workgroups; rows of db_partial
+};
+NarrowShape narrow_shape(int64_t rows, int64_t k, int64_t n, bool gated, bool activated);
+hipError_t launch_narrow(int type, const NarrowArgs& a, bool gated, const NarrowShape& p, hipStream_t s);
+
 // dst[r][c] = src[r * s_row + c * s_col] for c < cols, 0 for c in [cols, ld_dst): an operand in the layout the
 // tiled product reads.  src_type / dst_type: gs_type.  sums (may be null; not for GS_TYPE_E4M3): column sums of
 // the unrounded values per block of rows, [pack_row_blocks(rows)][cols].

@@ -242,6 +242,7 @@ struct BackwardPlan {
     int64_t kp, np;    // padded widths of x / weight copies and of dz
     Tiling tz, tx, tw;
     int64_t strips;    // rows of the column sums' partials out of the z product or the copy of dy
+    NarrowShape narrow;  // kp != 0: one kernel for everything
     void *x, *w, *dz, *sums, *sums2, *partial;
     size_t bytes;
 };
@@ -251,6 +252,14 @@ BackwardPlan plan_backward(const gs_linear_desc* d, const Dims& o, bool gated, v
     std::memset(&p, 0, sizeof(p));
     Carver c{static_cast<char*>(ws)};
     const int es = elem_bytes(d->type);
+    if (!o.pack_x && !o.pack_w) p.narrow = narrow_shape(o.m, o.k, o.n, gated, d->act != GS_ACT_NONE);
+    if (p.narrow.kp) {
+        p.partial = c.take((size_t)p.narrow.groups * o.n * o.k * 4);
+        p.sums = c.take((size_t)p.narrow.db_rows * o.n * 4);
+        p.sums2 = c.take(colsum_partial_floats(p.narrow.db_rows, (int32_t)o.n) * 4);
+        p.bytes = c.used;
+        return p;
+    }
     p.need_z = gated || d->act != GS_ACT_NONE;
     p.need_dz = p.need_z || d->y_type != d->type || d->y_channel_major || o.n % 8 != 0 || o.ld_y % 8 != 0 || o.ld_y >= (1 << 21);
     p.kp = round8(o.k);
@@ -288,6 +297,29 @@ gs_status backward(const gs_linear_desc* d, bool gated, const void* x, const voi
     const bool cm = d->y_channel_major != 0;
     hipError_t e = hipSuccess;
 
+    if (p.narrow.kp) {
+        if (!dx && !dweight && !dbias) return GS_OK;
+        NarrowArgs a;
+        std::memset(&a, 0, sizeof(a));
+        a.x = x, a.w = weight, a.ldx = o.ld_x, a.ldw = o.ld_w;
+        a.rows = d->rows, a.k = d->in, a.n = (int32_t)o.n;
+        a.bias = bias, a.act = d->act;
+        a.dy = dy, a.dy_type = d->y_type, a.d_si = cm ? 1 : o.ld_y, a.d_sj = cm ? o.ld_y : 1;
+        a.dx = dx, a.ld_dx = o.ld_r, a.dx_vec = o.ld_r % 4 == 0 && reinterpret_cast<uintptr_t>(dx) % 8 == 0;
+        a.dw_partial = dweight ? static_cast<float*>(p.partial) : nullptr;
+        a.db_partial = dbias ? static_cast<float*>(p.sums) : nullptr;
+        e = launch_narrow(d->type, a, gated, p.narrow, s);
+        if (e == hipSuccess && dweight) {
+            GemmArgs g;
+            std::memset(&g, 0, sizeof(g));
+            g.I = (int32_t)o.n, g.J = d->in, g.splits = p.narrow.groups, g.partial = a.dw_partial;
+            g.e.y = dweight, g.e.y_si = o.k, g.e.y_sj = 1, g.e.y_type = d->grad_type;
+            e = launch_gemm_reduce(g, s);
+        }
+        if (e == hipSuccess && dbias)
+            e = launch_colsum(p.sums, GS_TYPE_F32, o.n, p.narrow.db_rows, (int32_t)o.n, static_cast<float*>(p.sums2), dbias, s);
+        return launched(e, "backward of a narrow map");
+    }
     if (o.m > 0 && o.pack_x && (p.need_z || dweight)) {
         e = launch_pack(x, d->type, o.ld_x, 1, o.m, d->in, p.x, d->type, p.kp, nullptr, s);
         if (e != hipSuccess) return launched(e, "operand copy");

@@ -477,3 +477,53 @@ def test_large_offsets(env):
     within(torch, dw, dz.t() @ x[at].double(), 100 * 2.0 ** -23 * (dz.abs().t() @ x[at].double().abs()), "dweight")
     want = dz @ w.double()
     within(torch, dx[at], want, (2.0 ** -8 + 50 * 2.0 ** -23) * (dz.abs() @ w.double().abs()) + 1e-38, "dx")
+
+
+NARROW = [  # rows, in, out (hidden), gated, act, y, bias, channel_major
+    (4096, 64, 59, False, "none", "f32", True, True),
+    (5003, 64, 59, False, "none", "bf16", True, False),
+    (4100, 8, 3, False, "silu", "bf16", True, False),
+    (9001, 40, 100, False, "gelu", "bf16", True, False),
+    (4130, 64, 250, False, "none", "f32", False, True),
+    (4130, 56, 256, False, "relu", "bf16", True, False),
+    (6007, 120, 60, False, "silu", "f16", False, False),
+    (6007, 128, 128, False, "none", "f16", True, False),
+    (4097, 72, 17, False, "gelu", "f32", True, True),
+    (4099, 64, 128, True, "silu", "bf16", True, False),
+    (4099, 64, 100, True, "none", "bf16", False, False),
+    (4160, 24, 30, True, "gelu", "f16", True, False),
+    (70000, 64, 16, True, "silu", "bf16", True, False),
+    (4111, 128, 64, True, "relu", "f16", False, False),
+    (4111, 96, 33, True, "silu", "bf16", True, False),
+]
+
+
+@pytest.mark.parametrize("rows,k,n,gated,act,ytype,bias,cm", NARROW)
+def test_narrow_backward(env, rows, k, n, gated, act, ytype, bias, cm):
+    """Many rows of a narrow map: the backward in one pass over the rows."""
+    torch, gsmi, neural = env
+    dtype = "f16" if ytype == "f16" else "bf16"
+    w_rows = 2 * n if gated else n
+    normal, x, w, b, _, _, x64, w64, z, e_z = make_product(torch, rows, k, w_rows, dtype, 19 * rows + k, bias)
+    dy = normal(*((n, rows) if cm else (rows, n))).to(dt(torch, ytype))
+    d64 = dy.double().t() if cm else dy.double()
+    if gated:
+        g, u, a, d, e_g, e_u, e_a = gated_parts(torch, z, e_z, n, act)
+        dgate, e_gate = dz_bounds(torch, d64 * u, g, e_g, act)
+        e_gate = e_gate + d64.abs() * e_u * (d.abs() + 0.8 * e_g + 4e-6 * (1 + g.abs())) + 2.0 ** -22 * dgate.abs()
+        dz = torch.cat([dgate, d64 * a], 1)
+        e_dz = torch.cat([e_gate, d64.abs() * e_a + 2.0 ** -23 * (d64 * a).abs()], 1)
+        make = lambda gt: neural.GatedUnit(rows, k, n, dt(torch, dtype), act=act, grad_dtype=gt, backward=True)  # noqa: E731
+    else:
+        dz, e_dz = dz_bounds(torch, d64, z, e_z, act)
+        make = lambda gt: neural.Linear(rows, k, n, dt(torch, dtype), act=act, y_dtype=dt(torch, ytype), channel_major=cm,  # noqa: E731
+                                        grad_dtype=gt, backward=True)
+    plan = make(torch.float32)
+    dx, dw, db = plan.backward(x, w, dy, b)
+    check_grads(torch, dtype, "f32", x64, w64, dz, e_dz, dx, dw, db)
+    first = [t.clone() for t in (dx, dw)]
+    assert all(torch.equal(p, q) for p, q in zip(first, plan.backward(x, w, dy, b)))
+    assert torch.equal(make(dt(torch, dtype)).backward(x, w, dy, b)[1], dw.to(dt(torch, dtype)))
+    # views with rows further apart, NaN between them
+    xs, ws, dys = strided(torch, x, 8), strided(torch, w, 16), strided(torch, dy, 4)
+    assert all(torch.equal(p, q) for p, q in zip(first, plan.backward(xs, ws, dys, b)))
