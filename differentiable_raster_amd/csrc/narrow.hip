@@ -34,41 +34,58 @@ struct F16 {
 
 // An array of rows of RB bytes in LDS, read along its rows and, transposed, along its columns: the 32-byte
 // granule g of row r is kept at g ^ swizzle(r), so that neither way makes the rows of one read meet in a bank.
+// Every address is a lane's base, the same for all reads of one way, with some granule bits flipped and a
+// multiple of 16 or 32 rows added.
 template <int RB>
 struct Rows {
+    int32_t along_, across_, put_;
+    static constexpr int kUp = RB == 128 ? 64 : 128;  // what four rows further flip
     static __device__ __forceinline__ int swizzle(int r) { return RB == 128 ? (r >> 1) & 3 : r & 7; }
     static __device__ __forceinline__ int at(int r, int byte) { return r * RB + (((byte >> 5) ^ swizzle(r)) << 5) + (byte & 31); }
-    // 16 rows from r0 on, 32 columns from 32 kk on: lane l holds row l & 15, 8 columns of its quarter
-    static __device__ __forceinline__ u32x4 along(const char* p, int r0, int kk, int lane) {
-        return *reinterpret_cast<const u32x4*>(p + at(r0 + (lane & 15), kk * 64 + (lane >> 4) * 16));
+    __device__ __forceinline__ void init(int lane) {
+        const int l = lane & 15, q = lane >> 4;
+        along_ = at(l, q * 16);
+        across_ = at(q * 8 + (l >> 2), (l & 3) * 8);
+        put_ = at(l, q * 8);
+    }
+    // Keeps the compiler from holding an address per read over the loop, for which there are no registers.
+    __device__ __forceinline__ void renew() { asm volatile("" : "+v"(along_), "+v"(across_), "+v"(put_)); }
+    // 16 rows from r0 (a multiple of 16) on, 32 columns from 32 kk on: lane l holds row l & 15, 8 columns of its quarter
+    __device__ __forceinline__ u32x4 along(const char* p, int r0, int kk) const {
+        return *reinterpret_cast<const u32x4*>(p + r0 * RB + (along_ ^ (kk << 6)));
     }
     // 16 columns (granule g), summed over 32 rows from 32 kk on: lane l holds column l & 15, 8 rows of its quarter
-    static __device__ __forceinline__ u32x4 across(const char* p, int g, int kk, int lane) {
-        const int l = lane & 15, r = kk * 32 + (lane >> 4) * 8 + (l >> 2), b = g * 32 + (l & 3) * 8;
+    __device__ __forceinline__ u32x4 across(const char* p, int g, int kk) const {
         typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + at(r, b)));
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + at(r + 4, b)));
+        const char* r = p + kk * 32 * RB;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(r + (across_ ^ (g << 5))));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(r + 4 * RB + (across_ ^ (g << 5) ^ kUp)));
         const u32x2 u = __builtin_bit_cast(u32x2, lo), v = __builtin_bit_cast(u32x2, hi);
         return u32x4{u[0], u[1], v[0], v[1]};
+    }
+    // lane l writes four neighbours of row r0 + (l & 15), columns 16 g + 4 (l >> 4) on
+    __device__ __forceinline__ void put(char* p, int r0, int g, u32x2 v) const {
+        *reinterpret_cast<u32x2*>(p + r0 * RB + (put_ ^ (g << 5))) = v;
     }
 };
 
 enum NarrowKind { kPlain = 0, kActivated = 1, kPaired = 2 };
 
-// Workgroups that share a CU: two where the fragments, accumulators and dy fit 128 registers.
+// Workgroups of eight waves that share a CU: two where 128 registers hold the fragments, accumulators and dy.
 constexpr int per_cu(int kp, int np, int kind) { return kp * np == 64 * 64 || (kp * np == 64 * 128 && kind == kPlain) ? 2 : 1; }
 
 // KP columns of x and NP weight rows at most; the paired kind keeps gates in rows 0..NP/2-1 and ups above.
 template <class T, int KP, int NP, int KIND>
 __global__ __launch_bounds__(kThreads, 2 * per_cu(KP, NP, KIND)) void narrow_kernel(NarrowArgs a) {
 #ifdef __HIP_DEVICE_COMPILE__
+    constexpr int WAVES = kThreads / 64;
     constexpr bool PAIRED = KIND == kPaired;
     typedef Rows<KP * 2> X;
     typedef Rows<NP * 2> Z;
-    constexpr int W_BYTES = NP * KP * 2, Z_BYTES = kRows * NP * 2;
-    __shared__ __align__(1024) char x0[kRows * KP * 2], x1[kRows * KP * 2];
-    __shared__ __align__(1024) char zs[W_BYTES > Z_BYTES ? W_BYTES : Z_BYTES];  // the weights at first
-    typedef __attribute__((address_space(3))) void lds_void;
+    constexpr int X_BYTES = kRows * KP * 2, Z_BYTES = kRows * NP * 2;
+    static_assert(NP * KP * 2 <= 2 * Z_BYTES, "");
+    __shared__ __align__(1024) char xs[3 * X_BYTES];
+    __shared__ __align__(1024) char zs[2 * Z_BYTES];  // the weights at first
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), q = lane >> 4, l = lane & 15;
     const int32_t nblk = (int32_t)(((int64_t)a.rows + kRows - 1) / kRows);
@@ -82,13 +99,19 @@ __global__ __launch_bounds__(kThreads, 2 * per_cu(KP, NP, KIND)) void narrow_ker
 
     // ---- roles of the waves ----
     constexpr int PF = PAIRED ? NP / 32 : NP / 16;           // columns of z in blocks of 16 (pairs)
-    constexpr int CZ = PF > 8 ? PF / 8 : 1, WPF = PF < 8 ? 8 / PF : 1, RZ = 4 / WPF;
-    constexpr int KF = KP / 16, WPK = 8 / KF, RX = 4 / WPK;  // columns of dx; waves per column; row blocks per wave
-    constexpr int NF = NP / 16, NW = NF >= 8 ? NF / 8 : 1, KW = NF >= 8 ? KF : KF * NF / 8;  // dW blocks of a wave
-    const int cz0 = PF >= 8 ? wave * CZ : wave % PF, rz0 = PF >= 8 ? 0 : wave / PF * RZ;
+    constexpr int CZ = PF > WAVES ? PF / WAVES : 1, WPF = PF < WAVES ? (WAVES / PF < 4 ? WAVES / PF : 4) : 1, RZ = 4 / WPF;
+    constexpr int KF = KP / 16, WPK = WAVES / KF, RX = 4 / WPK;  // columns of dx; waves per column; row blocks per wave
+    constexpr int NF = NP / 16, NW = NF >= WAVES ? NF / WAVES : 1, KW = NF >= WAVES ? KF : KF * NF / WAVES;  // dW blocks
+    static_assert(RX * WPK == 4 && KW > 0 && PF * WPF <= WAVES * CZ, "");
+    const bool has_z = wave * CZ < PF * WPF;  // waves beyond the blocks of z take part in the products alone
+    const int cz0 = PF >= WAVES ? wave * CZ : wave % PF, rz0 = PF >= WAVES ? 0 : wave / PF * RZ;
     const int kx = wave % KF, rx0 = wave / KF * RX;
-    const int nw0 = NF >= 8 ? wave * NW : wave % NF, kw0 = NF >= 8 ? 0 : wave / NF * KW;
+    const int nw0 = NF >= WAVES ? wave * NW : wave % NF, kw0 = NF >= WAVES ? 0 : wave / NF * KW;
 
+    X X_;
+    Z Z_;
+    X_.init(lane);
+    Z_.init(lane);
     // ---- the weights, once: through LDS into the fragments that this wave needs of them ----
     for (int id = tid; id < NP * (KP / 8); id += kThreads) {
         const int n = id / (KP / 8), c = id % (KP / 8), s = source(n);
@@ -105,7 +128,7 @@ __global__ __launch_bounds__(kThreads, 2 * per_cu(KP, NP, KIND)) void narrow_ker
         for (int h = 0; h < (PAIRED ? 2 : 1); h++) {
             const int n0 = h * (NP / 2) + (cz0 + c) * 16;
 #pragma unroll
-            for (int kk = 0; kk < KP / 32; kk++) wz[c][h][kk] = X::along(zs, n0, kk, lane);
+            for (int kk = 0; kk < KP / 32; kk++) wz[c][h][kk] = X_.along(zs, n0, kk);
 #pragma unroll
             for (int k = 0; k < 4; k++) {
                 const int s = source(n0 + q * 4 + k);
@@ -113,7 +136,7 @@ __global__ __launch_bounds__(kThreads, 2 * per_cu(KP, NP, KIND)) void narrow_ker
             }
         }
 #pragma unroll
-    for (int kk = 0; kk < NP / 32; kk++) wx[kk] = X::across(zs, kx, kk, lane);
+    for (int kk = 0; kk < NP / 32; kk++) wx[kk] = X_.across(zs, kx, kk);
 
     f32x4 dw[NW][KW];
     float db[CZ][PAIRED ? 2 : 1][4];
@@ -128,69 +151,71 @@ __global__ __launch_bounds__(kThreads, 2 * per_cu(KP, NP, KIND)) void narrow_ker
 #pragma unroll
             for (int k = 0; k < 4; k++) db[c][h][k] = 0.0f;
 
-    // ---- loads of a block: x to LDS without passing a register (rows past the end arrive as zeros), dy to registers
-    constexpr int XN = kRows * KP * 2 / 16 / kThreads;
-    auto fetch_x = [&](char* xs, int32_t blk) {
-        const int64_t r0 = (int64_t)blk * kRows;
-        const int32_t rows = a.rows - r0 < kRows ? (int32_t)(a.rows - r0) : kRows;
-        const char* base = static_cast<const char*>(a.x) + r0 * a.ldx * 2;
-        const __amdgpu_buffer_rsrc_t rs =
-            __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, (int32_t)(((int64_t)(rows - 1) * a.ldx + a.k) * 2), 0x00020000);
+    // ---- loads of a block into registers: x on its way to LDS, and dy; rows past the end are zeros
+    constexpr int XN = X_BYTES / 16 / kThreads;
+    static_assert(X_BYTES / 16 % kThreads == 0, "");
+    u32x4 xr[XN];
+    auto fetch_x = [&](int32_t blk) {
 #pragma unroll
         for (int n = 0; n < XN; n++) {
-            const int id = tid + n * kThreads, r = id / (KP / 8), slot = id % (KP / 8);
-            const int c = ((slot >> 1) ^ X::swizzle(r)) * 2 + (slot & 1);
-            const int32_t off = r < rows && c * 8 < a.k ? (int32_t)(r * a.ldx * 2 + c * 16) : 0x7FFFFFF0;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(xs + (n * kThreads + wave * 64) * 16), 16, off, 0, 0, 0);
+            const int id = tid + n * kThreads, c = id % (KP / 8) * 8;
+            const int64_t r = (int64_t)blk * kRows + id / (KP / 8);
+            u32x4 v = {0u, 0u, 0u, 0u};
+            if (r < a.rows && c < a.k) v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.x) + r * a.ldx + c);
+            xr[n] = v;
+        }
+    };
+    auto store_x = [&](char* to) {
+#pragma unroll
+        for (int n = 0; n < XN; n++) {
+            const int id = tid + n * kThreads;
+            *reinterpret_cast<u32x4*>(to + X::at(id / (KP / 8), id % (KP / 8) * 16)) = xr[n];
         }
     };
     const bool vec = a.d_sj == 1 && (a.d_si & 3) == 0 && (H & 3) == 0;
     f32x4 dy[RZ][CZ];
-    auto fetch_dy_as = [&](auto type, int32_t blk) {
+    int64_t dy_lane = ((int64_t)rz0 * 16 + l) * a.d_si + ((int64_t)cz0 * 16 + q * 4) * a.d_sj;
+    int64_t dx_lane = ((int64_t)rx0 * 16 + l) * a.ld_dx + kx * 16 + q * 4;
+    // in whole vectors, or element by element where strides or the width ask for it
+    auto fetch_dy_as = [&](auto type, auto vectors, int32_t blk) {
 #pragma unroll
-        for (int r = 0; r < RZ; r++)
+        for (int r = 0; r < RZ; r++) {
+            const bool in = (int64_t)blk * kRows + (rz0 + r) * 16 + l < a.rows;
 #pragma unroll
             for (int c = 0; c < CZ; c++) {
-                const int64_t i = (int64_t)blk * kRows + (rz0 + r) * 16 + l;
                 const int32_t j = (cz0 + c) * 16 + q * 4;
-                const int64_t at = i * a.d_si + j * a.d_sj;
+                const int64_t at = dy_lane + ((int64_t)blk * kRows + r * 16) * a.d_si + c * 16 * a.d_sj;
                 f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (i < a.rows && j < H) {
-                    if (vec) {
-                        v = load_elem4(a.dy, decltype(type)::value, at);
-                    } else {
+                if (decltype(vectors)::value) {
+                    if (in && j < H) v = load_elem4(a.dy, decltype(type)::value, at);
+                } else {
 #pragma unroll
-                        for (int k = 0; k < 4; k++)
-                            if (j + k < H) v[k] = load_elem(a.dy, decltype(type)::value, at + k * a.d_sj);
-                    }
+                    for (int k = 0; k < 4; k++)
+                        if (in && j + k < H) v[k] = load_elem(a.dy, decltype(type)::value, at + k * a.d_sj);
                 }
                 dy[r][c] = v;
             }
+        }
+    };
+    auto fetch_dy_type = [&](auto type, int32_t blk) {
+        if (vec)
+            fetch_dy_as(type, std::true_type(), blk);
+        else
+            fetch_dy_as(type, std::false_type(), blk);
     };
     auto fetch_dy = [&](int32_t blk) {
+        if (!has_z) return;
         if (a.dy_type == GS_TYPE_F32)
-            fetch_dy_as(std::integral_constant<int, GS_TYPE_F32>(), blk);
+            fetch_dy_type(std::integral_constant<int, GS_TYPE_F32>(), blk);
         else if (a.dy_type == GS_TYPE_BF16)
-            fetch_dy_as(std::integral_constant<int, GS_TYPE_BF16>(), blk);
+            fetch_dy_type(std::integral_constant<int, GS_TYPE_BF16>(), blk);
         else
-            fetch_dy_as(std::integral_constant<int, GS_TYPE_F16>(), blk);
+            fetch_dy_type(std::integral_constant<int, GS_TYPE_F16>(), blk);
     };
 
-    auto block = [&](char* xs, char* next, int32_t blk) {
-        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this block's x is in LDS, which the barrier alone does not wait for
-        __syncthreads();
-        f32x4 d[RZ][CZ];
-#pragma unroll
-        for (int r = 0; r < RZ; r++)
-#pragma unroll
-            for (int c = 0; c < CZ; c++) d[r][c] = dy[r][c];
-        int ln = lane;  // addresses are computed again per block: held over the loop they cost more than they save
-        asm volatile("" : "+v"(ln));
-        const int32_t after = blk + gridDim.x;
-        if (after < nblk) {
-            fetch_x(next, after);
-            fetch_dy(after);
-        }
+    // dz of block blk, from its x in xb, into zb; then dy of the block after it
+    auto make_dz = [&](const char* xb, char* zb, int32_t blk, int32_t then) {
+        if (!has_z) return;
         // dz into LDS
         f32x4 z[RZ][CZ], u[RZ][CZ];
         if (KIND != kPlain) {
@@ -205,7 +230,7 @@ __global__ __launch_bounds__(kThreads, 2 * per_cu(KP, NP, KIND)) void narrow_ker
                     }
 #pragma unroll
                 for (int kk = 0; kk < KP / 32; kk++) {
-                    const u32x4 fx = X::along(xs, (rz0 + r) * 16, kk, ln);
+                    const u32x4 fx = X_.along(xb, (rz0 + r) * 16, kk);
 #pragma unroll
                     for (int c = 0; c < CZ; c++) {
                         z[r][c] = T::mma(wz[c][0][kk], fx, z[r][c]);
@@ -214,59 +239,69 @@ __global__ __launch_bounds__(kThreads, 2 * per_cu(KP, NP, KIND)) void narrow_ker
                 }
             }
         }
-        auto finish = [&](auto act) {
+        // whole: no row and no column of this wave's blocks lies outside
+        auto finish = [&](auto act, auto whole) {
 #pragma unroll
             for (int r = 0; r < RZ; r++) {
-                const int row = (rz0 + r) * 16 + (ln & 15);
-                const bool in = (int64_t)blk * kRows + row < a.rows;
+                const bool in = decltype(whole)::value || (int64_t)blk * kRows + (rz0 + r) * 16 + l < a.rows;
 #pragma unroll
                 for (int c = 0; c < CZ; c++) {
-                    const int j = (cz0 + c) * 16 + (ln >> 4) * 4;
+                    const int j = (cz0 + c) * 16 + q * 4;
                     float dg[4], du[4];
 #pragma unroll
                     for (int k = 0; k < 4; k++) {
                         float v = 0.0f, dv = 1.0f;
                         if (KIND != kPlain) act_both(z[r][c][k], decltype(act)::value, v, dv);
-                        const bool keep = in && j + k < H;
-                        dg[k] = PAIRED ? d[r][c][k] * u[r][c][k] * dv : d[r][c][k] * dv;
+                        const bool keep = decltype(whole)::value || (in && j + k < H);
+                        dg[k] = PAIRED ? dy[r][c][k] * u[r][c][k] * dv : KIND == kPlain ? dy[r][c][k] : dy[r][c][k] * dv;
                         dg[k] = keep ? dg[k] : 0.0f;
                         db[c][0][k] += dg[k];
                         if (PAIRED) {
-                            du[k] = keep ? d[r][c][k] * v : 0.0f;
+                            du[k] = keep ? dy[r][c][k] * v : 0.0f;
                             db[c][PAIRED ? 1 : 0][k] += du[k];
                         }
                     }
-                    *reinterpret_cast<u32x2*>(zs + Z::at(row, j * 2)) = u32x2{pack2(dg[0], dg[1], T::type), pack2(dg[2], dg[3], T::type)};
+                    Z_.put(zb, (rz0 + r) * 16, cz0 + c, u32x2{pack2(dg[0], dg[1], T::type), pack2(dg[2], dg[3], T::type)});
                     if (PAIRED)
-                        *reinterpret_cast<u32x2*>(zs + Z::at(row, NP + j * 2)) =
-                            u32x2{pack2(du[0], du[1], T::type), pack2(du[2], du[3], T::type)};
+                        Z_.put(zb, (rz0 + r) * 16, NP / 32 + cz0 + c, u32x2{pack2(du[0], du[1], T::type), pack2(du[2], du[3], T::type)});
                 }
             }
         };
+        const bool whole = ((int64_t)blk + 1) * kRows <= a.rows && (cz0 + CZ) * 16 <= H;
+        auto choose = [&](auto act) {
+            if (whole)
+                finish(act, std::true_type());
+            else
+                finish(act, std::false_type());
+        };
         if (KIND == kPlain || a.act == GS_ACT_NONE)
-            finish(std::integral_constant<int, GS_ACT_NONE>());
+            choose(std::integral_constant<int, GS_ACT_NONE>());
         else if (a.act == GS_ACT_SILU)
-            finish(std::integral_constant<int, GS_ACT_SILU>());
+            choose(std::integral_constant<int, GS_ACT_SILU>());
         else if (a.act == GS_ACT_GELU)
-            finish(std::integral_constant<int, GS_ACT_GELU>());
+            choose(std::integral_constant<int, GS_ACT_GELU>());
         else
-            finish(std::integral_constant<int, GS_ACT_RELU>());
-        __syncthreads();
-        // dx: this wave's 16 columns of some of the rows
-        if (a.dx) {
+            choose(std::integral_constant<int, GS_ACT_RELU>());
+        if (then < nblk) fetch_dy(then);
+    };
+    // dx of block blk and its share of dweight
+    auto products = [&](const char* xb, const char* zb, int32_t blk) {
+        if (a.dx) {  // this wave's 16 columns of some of the rows
+            f32x4 acc[RX];
+#pragma unroll
+            for (int r = 0; r < RX; r++) acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int kk = 0; kk < NP / 32; kk++)
+#pragma unroll
+                for (int r = 0; r < RX; r++) acc[r] = T::mma(wx[kk], Z_.along(zb, (rx0 + r) * 16, kk), acc[r]);
 #pragma unroll
             for (int r = 0; r < RX; r++) {
-                f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int kk = 0; kk < NP / 32; kk++) acc = T::mma(wx[kk], Z::along(zs, (rx0 + r) * 16, kk, ln), acc);
-                const int64_t i = (int64_t)blk * kRows + (rx0 + r) * 16 + (ln & 15);
-                const int32_t j = kx * 16 + (ln >> 4) * 4;
-                if (i < a.rows && j < a.k) {
-                    uint16_t* o = static_cast<uint16_t*>(a.dx) + i * a.ld_dx + j;
+                if ((int64_t)blk * kRows + (rx0 + r) * 16 + l < a.rows && kx * 16 + q * 4 < a.k) {
+                    uint16_t* o = static_cast<uint16_t*>(a.dx) + dx_lane + ((int64_t)blk * kRows + r * 16) * a.ld_dx;
                     if (a.dx_vec) {
-                        *reinterpret_cast<u32x2*>(o) = u32x2{pack2(acc[0], acc[1], T::type), pack2(acc[2], acc[3], T::type)};
+                        *reinterpret_cast<u32x2*>(o) = u32x2{pack2(acc[r][0], acc[r][1], T::type), pack2(acc[r][2], acc[r][3], T::type)};
                     } else {
-                        for (int k = 0; k < 4; k++) o[k] = (uint16_t)pack2(acc[k], 0.0f, T::type);  // k is a multiple of 8
+                        for (int k = 0; k < 4; k++) o[k] = (uint16_t)pack2(acc[r][k], 0.0f, T::type);  // a.k is a multiple of 8
                     }
                 }
             }
@@ -276,9 +311,9 @@ __global__ __launch_bounds__(kThreads, 2 * per_cu(KP, NP, KIND)) void narrow_ker
             for (int kk = 0; kk < kRows / 32; kk++) {
                 u32x4 fn[NW], fk[KW];
 #pragma unroll
-                for (int n = 0; n < NW; n++) fn[n] = Z::across(zs, nw0 + n, kk, ln);
+                for (int n = 0; n < NW; n++) fn[n] = Z_.across(zb, nw0 + n, kk);
 #pragma unroll
-                for (int k = 0; k < KW; k++) fk[k] = X::across(xs, kw0 + k, kk, ln);
+                for (int k = 0; k < KW; k++) fk[k] = X_.across(xb, kw0 + k, kk);
 #pragma unroll
                 for (int n = 0; n < NW; n++)
 #pragma unroll
@@ -286,15 +321,38 @@ __global__ __launch_bounds__(kThreads, 2 * per_cu(KP, NP, KIND)) void narrow_ker
             }
         }
     };
-    int32_t blk = blockIdx.x;
+
+    // Between two barriers the dz of one block is made and the products of the block before it are taken, in one
+    // order by half of the waves of a SIMD and in the other by the other half, so that the activations' vector
+    // work runs beside the matrix and LDS work.  x is in LDS from one block ahead on.
+    const int32_t step = gridDim.x, first = blockIdx.x;
     __syncthreads();  // the weights' fragments are read: their memory is dz's from here on
-    if (blk < nblk) {
-        fetch_x(x0, blk);
-        fetch_dy(blk);
+    if (first < nblk) {
+        fetch_x(first);
+        fetch_dy(first);
+        store_x(xs);
     }
-    for (; blk < nblk; blk += 2 * gridDim.x) {
-        block(x0, x1, blk);
-        if (blk + (int32_t)gridDim.x < nblk) block(x1, x0, blk + gridDim.x);
+    if (first + step < nblk) fetch_x(first + step);
+    int at = 0;  // x buffer of the block whose products come next
+    // t: the block whose dz is made; the one before it is t - step
+    for (int32_t t = first, n = 0; t < nblk + step && first < nblk; t += step, n++) {
+        __syncthreads();
+        const int x_dz = n == 0 ? 0 : (at == 2 ? 0 : at + 1), x_new = x_dz == 2 ? 0 : x_dz + 1;
+        if (t + step < nblk) store_x(xs + x_new * X_BYTES);
+        if (t + 2 * step < nblk) fetch_x(t + 2 * step);
+#pragma unroll 1
+        for (int half = 0; half < 2; half++) {
+            X_.renew();
+            Z_.renew();
+            int32_t now = t;  // like the bases: what depends on it is worked out where it is used
+            asm volatile("" : "+v"(dy_lane), "+v"(dx_lane), "+s"(now));
+            if (half == ((wave >> 2) & 1)) {
+                if (now < nblk) make_dz(xs + x_dz * X_BYTES, zs + (n & 1) * Z_BYTES, now, now + step);
+            } else {
+                if (n > 0) products(xs + at * X_BYTES, zs + ((n - 1) & 1) * Z_BYTES, now - step);
+            }
+        }
+        at = x_dz;
     }
 
     // ---- this workgroup's shares ----
@@ -310,8 +368,8 @@ __global__ __launch_bounds__(kThreads, 2 * per_cu(KP, NP, KIND)) void narrow_ker
             }
         }
     }
-    if (a.db_partial) {
-        float* o = a.db_partial + ((int64_t)blockIdx.x * WPF + (PF >= 8 ? 0 : wave / PF)) * a.n;
+    if (a.db_partial && has_z) {
+        float* o = a.db_partial + ((int64_t)blockIdx.x * WPF + (PF >= WAVES ? 0 : wave / PF)) * a.n;
 #pragma unroll
         for (int c = 0; c < CZ; c++)
 #pragma unroll
@@ -360,10 +418,10 @@ NarrowShape narrow_shape(int64_t rows, int64_t k, int64_t n, bool gated, bool ac
     p.kp = k <= 64 ? 64 : 128;
     p.np = width <= 64 ? 64 : width <= 128 ? 128 : 256;
     const int64_t blocks = (rows + kRows - 1) / kRows;
-    const int most = 256 * per_cu(p.kp, p.np, gated ? kPaired : activated ? kActivated : kPlain);
-    p.groups = (int)(blocks < most ? blocks : most);
+    const int together = per_cu(p.kp, p.np, gated ? kPaired : activated ? kActivated : kPlain), waves = kThreads / 64;
+    p.groups = (int)(blocks < 256 * together ? blocks : 256 * together);
     const int pf = gated ? p.np / 32 : p.np / 16;
-    p.db_rows = p.groups * (pf < 8 ? 8 / pf : 1);
+    p.db_rows = p.groups * (pf < waves ? (waves / pf < 4 ? waves / pf : 4) : 1);
     return p;
 }
 

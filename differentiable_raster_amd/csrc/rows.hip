@@ -513,8 +513,8 @@ hipError_t launch_few_rows(int type, EpiKind kind, bool aligned, const GemmArgs&
 }
 
 hipError_t launch_gemm_reduce(const GemmArgs& g, hipStream_t s) {
-    const int lanes = g.splits >= 32 ? 16 : g.splits >= 8 ? 4 : 1;
     const int64_t total = ((int64_t)g.J + 3) / 4 * g.I;
+    const int lanes = g.splits >= 128 && total < 16384 ? 64 : g.splits >= 32 ? 16 : g.splits >= 8 ? 4 : 1;
     int64_t blocks = (total + 256 / lanes - 1) / (256 / lanes);
     if (blocks > 8192) blocks = 8192;
     hipLaunchKernelGGL(reduce_kernel, dim3((unsigned)blocks), dim3(256), 0, s, g, lanes);
