@@ -41,6 +41,13 @@ struct TE4m3 {
         c = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(a0, b0, c, 0, 0, 0);
         return __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(a1, b1, c, 0, 0, 0);
     }
+    // 128 k at once, at twice the rate of the above: both chunks that a lane holds of a step; block scales of 1
+    static __device__ __forceinline__ f32x4 mma2(u32x4 a0, u32x4 a1, u32x4 b0, u32x4 b1, f32x4 c) {
+        typedef int32_t s32x8 __attribute__((ext_vector_type(8)));
+        const s32x8 a = {(int)a0[0], (int)a0[1], (int)a0[2], (int)a0[3], (int)a1[0], (int)a1[1], (int)a1[2], (int)a1[3]};
+        const s32x8 b = {(int)b0[0], (int)b0[1], (int)b0[2], (int)b0[3], (int)b1[0], (int)b1[1], (int)b1[2], (int)b1[3]};
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
+    }
 };
 
 // ---------------------------------------------------------------------------------------------------
@@ -377,30 +384,37 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
 #pragma unroll
         for (int j = 0; j < FJ; j++) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    constexpr int H = FI / 2;  // blocks of a in a quarter step
+    constexpr bool WHOLE = T::chunk == 16;  // a product takes the whole step of its rows
+    constexpr int PARTS = WHOLE && FI >= 4 ? 4 : 2, H = FI / PARTS;  // blocks of a whose fragments are held together
     Reader<BI, LA> reada;
     Reader<BJ, LB> readb;
     reada.init(wi * FI, lane);
     readb.init(wj * FJ, lane);
-    u32x4 fa[2][H], fb[2][FJ];
+    u32x4 fa[2][WHOLE ? 2 * H : H], fb[2][FJ];
     auto fetch = [&](char* ta, char* tb, int32_t kt) {
         const int64_t k = (int64_t)kt * BK;
         oa.load(ta, wave, pa, g.lda, k, ra, g.K - k);
         ob.load(tb, wave, pb, g.ldb, k, rb, g.K - k);
     };
-    auto read_a = [&](const char* ta, int kk, int half) {
+    auto read_a = [&](const char* ta, int kk, int part) {
 #pragma unroll
-        for (int i = 0; i < H; i++) fa[half][i] = reada.read(ta, half * H + i, kk);
+        for (int i = 0; i < H; i++) fa[part & 1][WHOLE ? kk * H + i : i] = reada.read(ta, part * H + i, kk);
     };
     auto read_b = [&](const char* tb, int kk) {
 #pragma unroll
         for (int j = 0; j < FJ; j++) fb[kk][j] = readb.read(tb, j, kk);
     };
-    auto multiply = [&](int kk, int half) {
+    auto multiply = [&](int kk, int part) {
 #pragma unroll
         for (int i = 0; i < H; i++)
 #pragma unroll
-            for (int j = 0; j < FJ; j++) acc[half * H + i][j] = T::mma(fb[kk][j], fa[half][i], acc[half * H + i][j]);
+            for (int j = 0; j < FJ; j++) {
+                f32x4& sum = acc[part * H + i][j];
+                if constexpr (WHOLE)
+                    sum = T::mma2(fb[0][j], fb[1][j], fa[part & 1][i], fa[part & 1][H + i], sum);
+                else
+                    sum = T::mma(fb[kk][j], fa[part][i], sum);
+            }
         __builtin_amdgcn_sched_barrier(0);
     };
     // Every load from memory to LDS has landed, and every wave is here.  The barrier alone would not wait for
@@ -415,6 +429,22 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
     auto step = [&](char* ta, char* tb, char* next_a, char* next_b, int32_t kt) {
         reada.renew();
         readb.renew();
+        if constexpr (WHOLE) {
+#pragma unroll
+            for (int p = 0; p + 1 < PARTS; p++) {
+                read_a(ta, 0, p + 1);
+                read_a(ta, 1, p + 1);
+                multiply(0, p);
+            }
+            landed();
+            if (kt + 2 < kt1) fetch(ta, tb, kt + 2);
+            read_a(next_a, 0, 0);
+            read_a(next_a, 1, 0);
+            multiply(0, PARTS - 1);
+            read_b(next_b, 0);
+            read_b(next_b, 1);
+            return;
+        }
         read_a(ta, 0, 1);
         multiply(0, 0);
         read_a(ta, 1, 0);
@@ -433,6 +463,10 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
     landed();
     read_a(a0, 0, 0);
     read_b(b0, 0);
+    if constexpr (WHOLE) {
+        read_a(a0, 1, 0);
+        read_b(b0, 1);
+    }
     int32_t kt = kt0;
     for (; kt + 2 <= kt1; kt += 2) {
         step(a0, b0, a1, b1, kt);
@@ -573,7 +607,9 @@ hipError_t launch_shape(Layout la, Layout lb, EpiKind kind, const GemmArgs& g, h
 template <class T>
 hipError_t launch_type(TileShape shape, Layout la, Layout lb, EpiKind kind, const GemmArgs& g, hipStream_t s) {
     switch (shape) {
-        case kTile256: return launch_shape<T, kTile256>(la, lb, kind, g, s);
+        case kTile256:  // 8-bit fragments of such a tile do not fit the registers
+            if constexpr (T::chunk == 8) return launch_shape<T, kTile256>(la, lb, kind, g, s);
+            return hipErrorInvalidValue;
         case kTile128: return launch_shape<T, kTile128>(la, lb, kind, g, s);
         case kTile64: return launch_shape<T, kTile64>(la, lb, kind, g, s);
         case kTile64x256: return launch_shape<T, kTile64x256>(la, lb, kind, g, s);
@@ -664,6 +700,117 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(GemmArgs g) {
         epi_linear(g.e, v[0], i, j, g.J);
 }
 
+// At most four rows: the matrix unit would leave three quarters of its rows empty and give a workgroup 16 rows
+// of b, which keeps most CUs idle where b has 1024 rows.  Here 64 lanes share one row of b (one gate and its up)
+// and `split` waves its summed axis, the sums are float32 multiply-adds.
+template <class T>
+__device__ __forceinline__ void chunk_values(u32x4 c, float (&v)[T::chunk]) {
+    if constexpr (T::chunk == 8) {
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const uint16_t h = (uint16_t)(c[k >> 1] >> ((k & 1) * 16));
+            v[k] = T::type == GS_TYPE_BF16 ? bf16_to_f32(h) : f16_to_f32(h);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(c[k], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(c[k], true);
+            v[4 * k] = lo[0], v[4 * k + 1] = lo[1], v[4 * k + 2] = hi[0], v[4 * k + 3] = hi[1];
+        }
+    }
+}
+
+constexpr int kHandful = 4;
+
+template <class T, int M, int EPI, bool ALIGNED>
+__global__ __launch_bounds__(256) void handful_kernel(GemmArgs g, int split) {
+    constexpr int NB = EPI == kEpiGated ? 2 : 1;
+    __shared__ float part[4][M * NB];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int32_t j = blockIdx.x * (4 / split) + wave / split, part_k = wave % split;
+    const bool jin = j < g.J;
+    const int ES = 16 / T::chunk;
+    float acc[M][NB];
+    for (int i = 0; i < M; i++)
+        for (int b = 0; b < NB; b++) acc[i][b] = 0.0f;
+    if (jin) {
+        const char* pb = static_cast<const char*>(g.b) + (int64_t)j * g.ldb * ES;
+        const int64_t up = (int64_t)g.J * g.ldb * ES;
+        const char* pa = static_cast<const char*>(g.a);
+        constexpr int U = M * NB <= 2 ? 4 : 2;  // chunks whose loads are in flight together
+        constexpr int STEP = 64 * T::chunk;
+        for (int64_t k0 = (int64_t)part_k * STEP * U; k0 < g.K; k0 += (int64_t)split * STEP * U) {
+            u32x4 fb[U][NB], fa[U][M];
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int64_t k = k0 + u * STEP + lane * T::chunk;
+#pragma unroll
+                for (int b = 0; b < NB; b++) fb[u][b] = row_chunk<T, ALIGNED>(pb + b * up, true, k, g.K);
+#pragma unroll
+                for (int i = 0; i < M; i++) fa[u][i] = row_chunk<T, ALIGNED>(pa + (int64_t)i * g.lda * ES, i < g.I, k, g.K);
+            }
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                float vb[NB][T::chunk];
+#pragma unroll
+                for (int b = 0; b < NB; b++) chunk_values<T>(fb[u][b], vb[b]);
+#pragma unroll
+                for (int i = 0; i < M; i++) {
+                    float va[T::chunk];
+                    chunk_values<T>(fa[u][i], va);
+#pragma unroll
+                    for (int b = 0; b < NB; b++)
+#pragma unroll
+                        for (int k = 0; k < T::chunk; k++) acc[i][b] = fmaf(va[k], vb[b][k], acc[i][b]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < M; i++)
+#pragma unroll
+        for (int b = 0; b < NB; b++) {
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) acc[i][b] += __shfl_xor(acc[i][b], m);
+            if (lane == 0) part[wave][i * NB + b] = acc[i][b];
+        }
+    __syncthreads();
+    if (part_k != 0 || !jin || lane >= g.I) return;
+    f32x4 v[NB];
+    for (int b = 0; b < NB; b++) {
+        float s = part[wave][lane * NB + b];
+        for (int w = 1; w < split; w++) s += part[wave + w][lane * NB + b];
+        v[b] = f32x4{s, 0.0f, 0.0f, 0.0f};
+    }
+    // one column: the epilogue's other three lie outside
+    const Epi& e = g.e;
+    float z = v[0][0], u = v[NB - 1][0];
+    if (e.scale_i) {
+        z *= e.scale_i[lane] * e.scale_j[j];
+        if (NB == 2) u *= e.scale_i[lane] * e.scale_j[g.J + j];
+    }
+    if (e.bias) {
+        z += e.bias[j];
+        if (NB == 2) u += e.bias[g.J + j];
+    }
+    z = act_value(z, e.act);
+    if (NB == 2) z *= u;
+    if (e.res) z += load_elem(e.res, e.y_type, lane * e.r_si + j * e.r_sj);
+    store_elem(e.y, e.y_type, lane * e.y_si + j * e.y_sj, z);
+}
+
+template <class T, int M, int EPI>
+hipError_t launch_handful(bool aligned, const GemmArgs& g, hipStream_t s) {
+    // waves per column: as many waves as the card holds in one go where columns are few
+    const int split = g.J >= 1024 ? 1 : g.J >= 512 ? 2 : 4;
+    const dim3 grid((unsigned)((g.J + 4 / split - 1) / (4 / split))), block(256);
+    if (aligned)
+        hipLaunchKernelGGL((handful_kernel<T, M, EPI, true>), grid, block, 0, s, g, split);
+    else
+        hipLaunchKernelGGL((handful_kernel<T, M, EPI, false>), grid, block, 0, s, g, split);
+    return hipGetLastError();
+}
+
 template <class T, int FI, int EPI>
 hipError_t launch_few_one(bool aligned, const GemmArgs& g, hipStream_t s) {
     const dim3 grid((unsigned)((g.J + 15) / 16)), block(kFewWaves * 64);
@@ -677,10 +824,14 @@ hipError_t launch_few_one(bool aligned, const GemmArgs& g, hipStream_t s) {
 template <class T>
 hipError_t launch_few_type(EpiKind kind, bool aligned, const GemmArgs& g, hipStream_t s) {
     if (kind == kEpiLinear) {
+        if (g.I == 1) return launch_handful<T, 1, kEpiLinear>(aligned, g, s);
+        if (g.I <= kHandful) return launch_handful<T, kHandful, kEpiLinear>(aligned, g, s);
         if (g.I <= 16) return launch_few_one<T, 1, kEpiLinear>(aligned, g, s);
         if (g.I <= 32) return launch_few_one<T, 2, kEpiLinear>(aligned, g, s);
         if (g.I <= 64) return launch_few_one<T, 4, kEpiLinear>(aligned, g, s);
     } else if (kind == kEpiGated) {
+        if (g.I == 1) return launch_handful<T, 1, kEpiGated>(aligned, g, s);
+        if (g.I <= kHandful) return launch_handful<T, kHandful, kEpiGated>(aligned, g, s);
         if (g.I <= 16) return launch_few_one<T, 1, kEpiGated>(aligned, g, s);
         if (g.I <= 32) return launch_few_one<T, 2, kEpiGated>(aligned, g, s);
         if (g.I <= 64) return launch_few_one<T, 4, kEpiGated>(aligned, g, s);

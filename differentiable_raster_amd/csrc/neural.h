@@ -110,11 +110,11 @@ struct NormArgs {
     // backward
     const void *dy, *ds;
     void* dx;
-    float* partial;  // [norm_groups(rows, width)][width]
+    float* partial;  // [norm_blocks(rows, width)][width]
 };
 hipError_t launch_norm_fwd(int type, const NormArgs& a, hipStream_t s);
-hipError_t launch_norm_bwd(int type, const NormArgs& a, int32_t groups, hipStream_t s);
-int32_t norm_groups(int64_t rows, int32_t width);
+hipError_t launch_norm_bwd(int type, const NormArgs& a, hipStream_t s);
+int32_t norm_blocks(int64_t rows, int32_t width);
 constexpr int kNormMaxWidth = 32768;
 
 }  // namespace gsmi

@@ -57,7 +57,7 @@ Tiling choose(int type, int64_t I, int64_t J, int64_t K, bool paired, bool may_s
     static const int held[kTileShapes] = {1, 2, 5, 2, 2};
     Tiling best{kTile64, 1, (int32_t)kt};
     double best_t = 1e300;
-    for (int s = 0; s < kTileShapes; s++) {
+    for (int s = type == GS_TYPE_E4M3 ? kTile128 : kTile256; s < kTileShapes; s++) {
         const TileDims d = kTileDims[s];
         const int64_t tiles = div_up(I, d.bi) * div_up(cols, d.bj);
         // a tile's own start and end: its first loads and its epilogue, whose bytes grow with its area
@@ -456,8 +456,8 @@ gs_status gs_quantize_rows(const gs_norm_desc* d, const void* x, void* q, float*
 size_t gs_rmsnorm_bwd_workspace_size(const gs_norm_desc* d) {
     NormArgs a;
     if (check_norm(d, &a) != GS_OK) return 0;
-    const int32_t groups = norm_groups(d->rows, d->width);
-    return align256((size_t)groups * d->width * 4) + align256(colsum_partial_floats(groups, d->width) * 4);
+    const int32_t blocks = norm_blocks(d->rows, d->width);
+    return align256((size_t)blocks * d->width * 4) + align256(colsum_partial_floats(blocks, d->width) * 4);
 }
 
 gs_status gs_rmsnorm_bwd(const gs_norm_desc* d, const void* s, const float* weight, const void* dy, const void* ds, void* dx,
@@ -470,10 +470,10 @@ gs_status gs_rmsnorm_bwd(const gs_norm_desc* d, const void* s, const float* weig
     if (!aligned_to(s, d->type) || !aligned_to(dy, d->type) || !aligned_to(ds, d->type) || !aligned_to(dx, d->type) ||
         !aligned_to(weight, GS_TYPE_F32) || !aligned_to(dweight, GS_TYPE_F32))
         BAD("an array is not aligned to its element");
-    const int32_t groups = norm_groups(d->rows, d->width);
+    const int32_t blocks = norm_blocks(d->rows, d->width);
     Carver c{static_cast<char*>(ws)};
-    float* partial = static_cast<float*>(c.take((size_t)groups * d->width * 4));
-    float* partial2 = static_cast<float*>(c.take(colsum_partial_floats(groups, d->width) * 4));
+    float* partial = static_cast<float*>(c.take((size_t)blocks * d->width * 4));
+    float* partial2 = static_cast<float*>(c.take(colsum_partial_floats(blocks, d->width) * 4));
     if (dweight) {
         st = check_ws(ws, ws_bytes, c.used);
         if (st != GS_OK) return st;
@@ -482,11 +482,11 @@ gs_status gs_rmsnorm_bwd(const gs_norm_desc* d, const void* s, const float* weig
     if (d->rows > 0) {
         a.s = const_cast<void*>(s), a.w = weight, a.dy = dy, a.ds = ds, a.dx = dx;
         a.partial = dweight ? partial : nullptr;
-        st = launched(launch_norm_bwd(d->type, a, groups, hs), "gs_rmsnorm_bwd launch");
+        st = launched(launch_norm_bwd(d->type, a, hs), "gs_rmsnorm_bwd launch");
         if (st != GS_OK) return st;
     }
     if (!dweight) return GS_OK;
-    return launched(launch_colsum(partial, GS_TYPE_F32, d->width, groups, d->width, partial2, dweight, hs), "weight gradient");
+    return launched(launch_colsum(partial, GS_TYPE_F32, d->width, blocks, d->width, partial2, dweight, hs), "weight gradient");
 }
 
 size_t gs_linear_workspace_size(const gs_linear_desc* d) { return forward_ws(d, false); }

@@ -196,13 +196,14 @@ __global__ __launch_bounds__(block_of(NT)) void norm_fwd_kernel(NormArgs a) {
 }
 
 // Each group of NT threads walks rows group, group + groups, ...; its columns' share of dweight stays in
-// registers and leaves once per group.
+// registers, and the shares of a workgroup's groups meet in LDS before they leave.
 template <class T, int NT, int NC>
-__global__ __launch_bounds__(block_of(NT)) void norm_bwd_kernel(NormArgs a, int32_t groups) {
+__global__ __launch_bounds__(block_of(NT)) void norm_bwd_kernel(NormArgs a) {
+    constexpr int RPB = rows_per_block(NT), WIDTH = NT * NC * 8;
     __shared__ float lds[16];
-    const int32_t group = blockIdx.x * rows_per_block(NT) + threadIdx.x / NT;
+    __shared__ float shares[RPB > 1 ? RPB * WIDTH : 1];
+    const int64_t group = (int64_t)blockIdx.x * RPB + threadIdx.x / NT, groups = (int64_t)gridDim.x * RPB;
     const int t = threadIdx.x % NT;
-    if (NT <= 64 && group >= groups) return;
     const bool vs = vec8(a.s, a.ld_s, a.width, T::type), vy = vec8(a.dy, a.ld_y, a.width, T::type);
     const bool vr = vec8(a.ds, a.ld_r, a.width, T::type), vx = vec8(a.dx, a.ld_x, a.width, T::type);
     float w[NC][8], acc[NC][8];
@@ -242,10 +243,22 @@ __global__ __launch_bounds__(block_of(NT)) void norm_bwd_kernel(NormArgs a, int3
             store8<T>(a.dx, row * a.ld_x, (c * NT + t) * 8, a.width, vx, g[c]);
         }
     }
-    if (a.partial) {
+    if (!a.partial) return;
+    if (RPB == 1) {
 #pragma unroll
         for (int c = 0; c < NC; c++)
-            store8<F32>(a.partial, (int64_t)group * a.width, (c * NT + t) * 8, a.width, (a.width & 7) == 0, acc[c]);
+            store8<F32>(a.partial, (int64_t)blockIdx.x * a.width, (c * NT + t) * 8, a.width, (a.width & 7) == 0, acc[c]);
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < NC; c++)
+#pragma unroll
+        for (int k = 0; k < 8; k++) shares[threadIdx.x / NT * WIDTH + (c * NT + t) * 8 + k] = acc[c][k];
+    __syncthreads();
+    for (int col = threadIdx.x; col < a.width; col += block_of(NT)) {
+        float s = 0.0f;
+        for (int w = 0; w < RPB; w++) s += shares[w * WIDTH + col];
+        a.partial[(int64_t)blockIdx.x * a.width + col] = s;
     }
 }
 
@@ -270,9 +283,8 @@ hipError_t fwd_one(const NormArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 template <class T, int NT, int NC>
-hipError_t bwd_one(const NormArgs& a, int32_t groups, hipStream_t s) {
-    const int blocks = (groups + rows_per_block(NT) - 1) / rows_per_block(NT);
-    hipLaunchKernelGGL((norm_bwd_kernel<T, NT, NC>), dim3((unsigned)blocks), dim3(block_of(NT)), 0, s, a, groups);
+hipError_t bwd_one(const NormArgs& a, int32_t blocks, hipStream_t s) {
+    hipLaunchKernelGGL((norm_bwd_kernel<T, NT, NC>), dim3((unsigned)blocks), dim3(block_of(NT)), 0, s, a);
     return hipGetLastError();
 }
 
@@ -286,13 +298,13 @@ hipError_t fwd_type(const NormArgs& a, hipStream_t s) {
     return r.nt == 256 ? fwd_one<T, 256, 4>(a, s) : fwd_one<T, 1024, 4>(a, s);
 }
 template <class T>
-hipError_t bwd_type(const NormArgs& a, int32_t groups, hipStream_t s) {
+hipError_t bwd_type(const NormArgs& a, int32_t blocks, hipStream_t s) {
     const RowShape r = row_shape(a.width);
-    if (r.nt == 8) return bwd_one<T, 8, 1>(a, groups, s);
-    if (r.nt == 16) return bwd_one<T, 16, 1>(a, groups, s);
-    if (r.nt == 32) return bwd_one<T, 32, 1>(a, groups, s);
-    if (r.nt == 64) return r.nc == 1 ? bwd_one<T, 64, 1>(a, groups, s) : bwd_one<T, 64, 4>(a, groups, s);
-    return r.nt == 256 ? bwd_one<T, 256, 4>(a, groups, s) : bwd_one<T, 1024, 4>(a, groups, s);
+    if (r.nt == 8) return bwd_one<T, 8, 1>(a, blocks, s);
+    if (r.nt == 16) return bwd_one<T, 16, 1>(a, blocks, s);
+    if (r.nt == 32) return bwd_one<T, 32, 1>(a, blocks, s);
+    if (r.nt == 64) return r.nc == 1 ? bwd_one<T, 64, 1>(a, blocks, s) : bwd_one<T, 64, 4>(a, blocks, s);
+    return r.nt == 256 ? bwd_one<T, 256, 4>(a, blocks, s) : bwd_one<T, 1024, 4>(a, blocks, s);
 }
 
 // ---- operand copies -------------------------------------------------------------------------------
@@ -450,17 +462,18 @@ hipError_t launch_norm_fwd(int type, const NormArgs& a, hipStream_t s) {
     return fwd_type<F32>(a, s);
 }
 
-// Groups of rows of the backward: enough to fill the card, few enough that their partial sums cost little.
-int32_t norm_groups(int64_t rows, int32_t width) {
-    const RowShape r = row_shape(width);
-    const int64_t most = (int64_t)2048 * rows_per_block(r.nt) / (r.nt >= 256 ? 2 : 1);
-    return (int32_t)(rows < most ? rows : most);
+// Workgroups of the backward: enough to fill the card, few enough that their partial sums cost little.
+int32_t norm_blocks(int64_t rows, int32_t width) {
+    const RowShape s = row_shape(width);
+    const int64_t blocks = (rows + rows_per_block(s.nt) - 1) / rows_per_block(s.nt), most = s.nt >= 256 ? 1024 : 2048;
+    return (int32_t)(blocks < most ? blocks : most);
 }
 
-hipError_t launch_norm_bwd(int type, const NormArgs& a, int32_t groups, hipStream_t s) {
-    if (type == GS_TYPE_BF16) return bwd_type<Bf16>(a, groups, s);
-    if (type == GS_TYPE_F16) return bwd_type<F16>(a, groups, s);
-    return bwd_type<F32>(a, groups, s);
+hipError_t launch_norm_bwd(int type, const NormArgs& a, hipStream_t s) {
+    const int32_t blocks = norm_blocks(a.rows, a.width);
+    if (type == GS_TYPE_BF16) return bwd_type<Bf16>(a, blocks, s);
+    if (type == GS_TYPE_F16) return bwd_type<F16>(a, blocks, s);
+    return bwd_type<F32>(a, blocks, s);
 }
 
 int64_t pack_row_blocks(int64_t rows) { return (rows + 63) / 64; }

@@ -18,7 +18,7 @@ ACTS = {"none": gsmi.GS_ACT_NONE, "relu": gsmi.GS_ACT_RELU, "silu": gsmi.GS_ACT_
 
 def _rows(t, name: str, rows: int, width: int, dtype):
     """(address, row stride) of a rows x width view."""
-    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width:
+    if t.dtype != dtype or t.shape != (rows, width):
         raise ValueError(f"{name}: expected {dtype} [{rows}, {width}], got {t.dtype} {list(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name}: device tensor expected")
@@ -33,7 +33,7 @@ def _rows(t, name: str, rows: int, width: int, dtype):
 def _vector(t, name: str, n: int):
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n:
+    if t.dtype != torch.float32 or t.shape != (n,):
         raise ValueError(f"{name}: expected torch.float32 [{n}], got {t.dtype} {list(t.shape)}")
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous device tensor expected")
@@ -123,7 +123,8 @@ class _Product:
         self.device = torch.device(device)
         self.desc = gsmi.gs_linear_desc(rows, n_in, n_out, TYPES[dtype], TYPES[self.y_dtype], TYPES[self.grad_dtype],
                                         ACTS[act], int(channel_major), n_in, n_in, 0, 0)
-        self.ws = None
+        self._y_shape = (n_out, rows) if channel_major else (rows, n_out)
+        self.ws, self._ws = None, (None, 0)
         self._y = self._grads = None
         self._reserve(backward)
 
@@ -133,13 +134,7 @@ class _Product:
         need = size(self.desc)
         if need and (self.ws is None or self.ws.numel() < need):
             self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-
-    def _ws(self):
-        return (None, 0) if self.ws is None else (self.ws.data_ptr(), self.ws.numel())
-
-    @property
-    def _y_shape(self):
-        return (self.n_out, self.rows) if self.channel_major else (self.rows, self.n_out)
+            self._ws = (self.ws.data_ptr(), need)
 
     def _operands(self, x, weight, backward):
         c, seen = self.desc, (self.desc.ld_x, self.desc.ld_w)
@@ -162,12 +157,12 @@ class _Product:
             out = self._y
         py, c.ld_y = _rows(out, "out", *self._y_shape, self.y_dtype)
         if self.gated:
-            gsmi.gs_gated(c, px, sx, pw, sw, pb, py, *self._ws(), stream)
+            gsmi.gs_gated(c, px, sx, pw, sw, pb, py, *self._ws, stream)
             return out
         pr = None
         if residual is not None:
             pr, c.ld_r = _rows(residual, "residual", *self._y_shape, self.y_dtype)
-        gsmi.gs_linear(c, px, sx, pw, sw, pb, pr, py, *self._ws(), stream)
+        gsmi.gs_linear(c, px, sx, pw, sw, pb, pr, py, *self._ws, stream)
         return out
 
     def backward(self, x, weight, dy, bias=None, stream=None):
@@ -186,7 +181,7 @@ class _Product:
         dx, dw, db = self._grads
         c.ld_r = self.n_in
         call = gsmi.gs_gated_bwd if self.gated else gsmi.gs_linear_bwd
-        call(c, px, pw, pb, p_dy, dx.data_ptr(), dw.data_ptr(), db.data_ptr() if pb else None, *self._ws(), stream)
+        call(c, px, pw, pb, p_dy, dx.data_ptr(), dw.data_ptr(), db.data_ptr() if pb else None, *self._ws, stream)
         return dx, dw, (db if pb else None)
 
 
