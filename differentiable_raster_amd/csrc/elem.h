@@ -21,6 +21,14 @@ __device__ __forceinline__ float f16_to_f32(uint16_t v) { return (float)__builti
 __device__ __forceinline__ uint16_t f32_to_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 __device__ __forceinline__ uint16_t f32_to_f16(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
 
+// 16 and 8 bytes at any address that is a multiple of the element: one wide access where the hardware has it.
+__device__ __forceinline__ u32x4 load16(const void* p) {
+    u32x4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+}
+__device__ __forceinline__ void store16(void* p, u32x4 v) { __builtin_memcpy(p, &v, 16); }
+
 // Element i of an array whose type is known at run time (uniform over the launch).
 __device__ __forceinline__ float load_elem(const void* p, int type, int64_t i) {
     if (type == GS_TYPE_F32) return static_cast<const float*>(p)[i];
@@ -37,10 +45,11 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, int type) {
     return type == GS_TYPE_BF16 ? (uint32_t)f32_to_bf16(a) | (uint32_t)f32_to_bf16(b) << 16
                                 : (uint32_t)f32_to_f16(a) | (uint32_t)f32_to_f16(b) << 16;
 }
-// Four consecutive elements from i on (the address is a multiple of their size).
+// Four or eight consecutive elements from i on.
 __device__ __forceinline__ f32x4 load_elem4(const void* p, int type, int64_t i) {
-    if (type == GS_TYPE_F32) return *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
-    const u32x2 v = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(p) + i);
+    if (type == GS_TYPE_F32) return __builtin_bit_cast(f32x4, load16(static_cast<const float*>(p) + i));
+    u32x2 v;
+    __builtin_memcpy(&v, static_cast<const uint16_t*>(p) + i, 8);
     f32x4 r;
     for (int k = 0; k < 4; k++) {
         const uint16_t h = (uint16_t)(v[k >> 1] >> ((k & 1) * 16));
@@ -50,13 +59,37 @@ __device__ __forceinline__ f32x4 load_elem4(const void* p, int type, int64_t i) 
 }
 __device__ __forceinline__ void store_elem4(void* p, int type, int64_t i, f32x4 v) {
     if (type == GS_TYPE_F32) {
-        *reinterpret_cast<f32x4*>(static_cast<float*>(p) + i) = v;
+        store16(static_cast<float*>(p) + i, __builtin_bit_cast(u32x4, v));
         return;
     }
-    u32x2 o;
-    o[0] = pack2(v[0], v[1], type);
-    o[1] = pack2(v[2], v[3], type);
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p) + i) = o;
+    const u32x2 o = {pack2(v[0], v[1], type), pack2(v[2], v[3], type)};
+    __builtin_memcpy(static_cast<uint16_t*>(p) + i, &o, 8);
+}
+__device__ __forceinline__ void load_elem8(const void* p, int type, int64_t i, float (&v)[8]) {
+    if (type == GS_TYPE_F32) {
+        const f32x4 a = load_elem4(p, type, i), b = load_elem4(p, type, i + 4);
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            v[k] = a[k];
+            v[4 + k] = b[k];
+        }
+    } else {
+        const u32x4 w = load16(static_cast<const uint16_t*>(p) + i);
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const uint16_t h = (uint16_t)(w[k >> 1] >> ((k & 1) * 16));
+            v[k] = type == GS_TYPE_BF16 ? bf16_to_f32(h) : f16_to_f32(h);
+        }
+    }
+}
+__device__ __forceinline__ void store_elem8(void* p, int type, int64_t i, const float (&v)[8]) {
+    if (type == GS_TYPE_F32) {
+        store_elem4(p, type, i, f32x4{v[0], v[1], v[2], v[3]});
+        store_elem4(p, type, i + 4, f32x4{v[4], v[5], v[6], v[7]});
+    } else {
+        store16(static_cast<uint16_t*>(p) + i,
+                u32x4{pack2(v[0], v[1], type), pack2(v[2], v[3], type), pack2(v[4], v[5], type), pack2(v[6], v[7], type)});
+    }
 }
 
 // 1 / (1 + e^-z): the reciprocal of infinity is 0, so large negative z give 0.

@@ -56,7 +56,7 @@ struct TE4m3 {
 __device__ __forceinline__ void epi_store(const Epi& e, int32_t i, int32_t j, int32_t J, f32x4 v) {
     const int64_t at = (int64_t)i * e.y_si + (int64_t)j * e.y_sj;
     const int32_t end = e.y_pad > J ? e.y_pad : J;
-    if (e.y_sj == 1 && (e.y_si & 3) == 0 && j + 4 <= end && (reinterpret_cast<uintptr_t>(e.y) & 15) == 0) {
+    if (e.y_sj == 1 && j + 4 <= end) {
         for (int k = 0; k < 4; k++)
             if (j + k >= J) v[k] = 0.0f;
         store_elem4(e.y, e.y_type, at, v);
@@ -68,7 +68,7 @@ __device__ __forceinline__ void epi_store(const Epi& e, int32_t i, int32_t j, in
 
 __device__ __forceinline__ f32x4 epi_load(const void* p, int type, int64_t si, int64_t sj, int32_t i, int32_t j, int32_t J) {
     const int64_t at = (int64_t)i * si + (int64_t)j * sj;
-    if (sj == 1 && (si & 3) == 0 && j + 4 <= J && (reinterpret_cast<uintptr_t>(p) & 15) == 0) return load_elem4(p, type, at);
+    if (sj == 1 && j + 4 <= J) return load_elem4(p, type, at);
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int k = 0; k < 4; k++)
         if (j + k < J) v[k] = load_elem(p, type, at + k * sj);
@@ -107,36 +107,21 @@ __device__ __forceinline__ void epi_gated(const Epi& e, f32x4 gate, f32x4 up, in
     epi_store(e, i, j, J, v);
 }
 // ---- the tiled product's epilogue: eight neighbours along j of row i, read back from LDS ----
-__device__ __forceinline__ bool vec8(const void* p, int type, int64_t si, int64_t sj) {
-    return sj == 1 && (si & (type == GS_TYPE_F32 ? 3 : 7)) == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
-}
-__device__ __forceinline__ void load8(const void* p, int type, int64_t at, int64_t sj, int32_t n, bool vec, float (&v)[8]) {
-    if (vec && n >= 8) {
-        const f32x4 a = load_elem4(p, type, at), b = load_elem4(p, type, at + 4);
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-            v[k] = a[k];
-            v[4 + k] = b[k];
-        }
+__device__ __forceinline__ void load8(const void* p, int type, int64_t at, int64_t sj, int32_t n, float (&v)[8]) {
+    if (sj == 1 && n >= 8) {
+        load_elem8(p, type, at, v);
     } else {
 #pragma unroll
         for (int k = 0; k < 8; k++) v[k] = k < n ? load_elem(p, type, at + k * sj) : 0.0f;
     }
 }
 // n of the eight values, zeros from there to `end`.
-__device__ __forceinline__ void store8(void* p, int type, int64_t at, int64_t sj, int32_t n, int32_t end, bool vec, const float (&v)[8]) {
-    if (vec && end >= 8) {
+__device__ __forceinline__ void store8(void* p, int type, int64_t at, int64_t sj, int32_t n, int32_t end, const float (&v)[8]) {
+    if (sj == 1 && end >= 8) {
         float o[8];
 #pragma unroll
         for (int k = 0; k < 8; k++) o[k] = k < n ? v[k] : 0.0f;
-        if (type == GS_TYPE_F32) {
-            f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(p) + at);
-            q[0] = f32x4{o[0], o[1], o[2], o[3]};
-            q[1] = f32x4{o[4], o[5], o[6], o[7]};
-        } else {
-            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + at) =
-                u32x4{pack2(o[0], o[1], type), pack2(o[2], o[3], type), pack2(o[4], o[5], type), pack2(o[6], o[7], type)};
-        }
+        store_elem8(p, type, at, o);
     } else {
 #pragma unroll
         for (int k = 0; k < 8; k++)
@@ -173,7 +158,7 @@ struct Columns {
 // s0, s1 collect the column sums.
 template <int EPI>
 __device__ __forceinline__ void epi8(const GemmArgs& g, float (&v)[8], float (&u)[8], const float (&d)[8], const Columns& cv,
-                                     const Columns& cu, int32_t i, int32_t j, bool vy, float (&s0)[8], float (&s1)[8]) {
+                                     const Columns& cu, int32_t i, int32_t j, float (&s0)[8], float (&s1)[8]) {
     const Epi& e = g.e;
     const int32_t n = g.J - j < 8 ? g.J - j : 8;
     const int64_t at = (int64_t)i * e.y_si + (int64_t)j * e.y_sj;
@@ -185,13 +170,13 @@ __device__ __forceinline__ void epi8(const GemmArgs& g, float (&v)[8], float (&u
 #pragma unroll
             for (int k = 0; k < 8; k++) v[k] += d[k];
         }
-        store8(e.y, e.y_type, at, e.y_sj, n, end, vy, v);
+        store8(e.y, e.y_type, at, e.y_sj, n, end, v);
     } else if (EPI == kEpiGated) {
         cu.apply(e, u, i);
         act8(v, e.act);
 #pragma unroll
         for (int k = 0; k < 8; k++) v[k] *= u[k];
-        store8(e.y, e.y_type, at, e.y_sj, n, n, vy, v);
+        store8(e.y, e.y_type, at, e.y_sj, n, n, v);
     } else {
         if (EPI == kEpiDz) {  // dz = dy act'(z)
             float da[8];
@@ -201,7 +186,7 @@ __device__ __forceinline__ void epi8(const GemmArgs& g, float (&v)[8], float (&u
                 v[k] = k < n ? d[k] * da[k] : 0.0f;
                 s0[k] += v[k];
             }
-            store8(e.y, e.y_type, at, e.y_sj, n, end, vy, v);
+            store8(e.y, e.y_type, at, e.y_sj, n, end, v);
         } else {  // dgate = dh up act'(gate) at column j, dup = dh act(gate) at column J + j
             cu.apply(e, u, i);
             float da[8];
@@ -214,11 +199,11 @@ __device__ __forceinline__ void epi8(const GemmArgs& g, float (&v)[8], float (&u
                 s0[k] += v[k];
                 s1[k] += u[k];
             }
-            store8(e.y, e.y_type, at, 1, n, n, vy, v);
+            store8(e.y, e.y_type, at, 1, n, n, v);
             // the padding of the whole row follows its last ups
             const int32_t over = n < 8 || j + 8 == g.J ? n + (e.y_pad - 2 * g.J) : n;
             const int32_t all = over < 8 ? over : 8;
-            store8(e.y, e.y_type, at + g.J, 1, n, all, vy && (g.J & 7) == 0, u);
+            store8(e.y, e.y_type, at + g.J, 1, n, all, u);
             for (int32_t c = 8; c < over; c++) store_elem(e.y, e.y_type, at + g.J + c, 0.0f);
         }
     }
@@ -489,8 +474,6 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
     char* room = BIG_A ? (object ? a1 : a0) : BIG_B ? (object ? b1 : b0) : object == 0 ? a0 : object == 1 ? a1 : object == 2 ? b0 : b1;
     f32x4* slab = reinterpret_cast<f32x4*>(room + wave % PER * ROOM);
     const int32_t iw = i0 + wi * TI, jw = j0 + wj * TJO, jl = jw + (lane % LPR) * 8;
-    const bool vy = vec8(g.e.y, g.e.y_type, g.e.y_si, g.e.y_sj), vd = vec8(g.e.dy, g.e.dy_type, g.e.d_si, g.e.d_sj);
-    const bool vr = vec8(g.e.res, g.e.y_type, g.e.r_si, g.e.r_sj);
     Columns cv, cu;
     cv.load(g.e, jl, g.J, 0);
     if (PAIRED) cu.load(g.e, jl, g.J, g.J);
@@ -519,9 +502,9 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
                     const int32_t i = ib + p * RPP;
                     const int32_t m = i < g.I ? n : 0;
                     if (EPI == kEpiLinear)
-                        load8(g.e.res, g.e.y_type, (int64_t)i * g.e.r_si + (int64_t)jl * g.e.r_sj, g.e.r_sj, m, vr, d[p]);
+                        load8(g.e.res, g.e.y_type, (int64_t)i * g.e.r_si + (int64_t)jl * g.e.r_sj, g.e.r_sj, m, d[p]);
                     else
-                        load8(g.e.dy, g.e.dy_type, (int64_t)i * g.e.d_si + (int64_t)jl * g.e.d_sj, g.e.d_sj, m, vd, d[p]);
+                        load8(g.e.dy, g.e.dy_type, (int64_t)i * g.e.d_si + (int64_t)jl * g.e.d_sj, g.e.d_sj, m, d[p]);
                 }
             }
 #pragma unroll
@@ -533,7 +516,7 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
                 float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
                 if (EPI == kEpiLinear && g.partial) {
                     float* o = g.partial + ((int64_t)blockIdx.z * g.I + i) * g.J;
-                    store8(o, GS_TYPE_F32, jl, 1, g.J - jl, g.J - jl, (g.J & 3) == 0, v);
+                    store8(o, GS_TYPE_F32, jl, 1, g.J - jl, g.J - jl, v);
                     continue;
                 }
                 float u[8];
@@ -546,7 +529,7 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
                         u[4 + k] = y[k];
                     }
                 }
-                epi8<EPI>(g, v, u, d[p], cv, cu, i, jl, vy, s0, s1);
+                epi8<EPI>(g, v, u, d[p], cv, cu, i, jl, s0, s1);
             }
         }
     };
@@ -623,11 +606,11 @@ hipError_t launch_type(TileShape shape, Layout la, Layout lb, EpiKind kind, cons
 // their ups) and its waves take turns along k; both operands go from memory straight to the registers of
 // the matrix instruction, and the waves' sums meet in LDS.
 // ---------------------------------------------------------------------------------------------------
-template <class T, bool ALIGNED>
+template <class T>
 __device__ __forceinline__ u32x4 row_chunk(const char* row, bool in, int64_t k, int64_t K) {
     u32x4 v = {0u, 0u, 0u, 0u};
     if (!in || k >= K) return v;
-    if (ALIGNED) return *reinterpret_cast<const u32x4*>(row + k * (16 / T::chunk));
+    if (k + T::chunk <= K) return load16(row + k * (16 / T::chunk));
     if (T::chunk == 8) {
         const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + k;
         for (int e = 0; e < 8; e++)
@@ -642,7 +625,7 @@ __device__ __forceinline__ u32x4 row_chunk(const char* row, bool in, int64_t k, 
 
 constexpr int kFewWaves = 8;
 
-template <class T, int FI, int EPI, bool ALIGNED>
+template <class T, int FI, int EPI>
 __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(GemmArgs g) {
     constexpr int NB = EPI == kEpiGated ? 2 : 1;
     constexpr int BK = 4 * T::chunk;  // k per step of a wave: one chunk per lane
@@ -670,9 +653,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(GemmArgs g) {
         for (int u = 0; u < U; u++) {
             const int64_t k = k0 + u * BK + (lane >> 4) * T::chunk;
 #pragma unroll
-            for (int b = 0; b < NB; b++) fb[u][b] = row_chunk<T, ALIGNED>(pb[b], jin, k, g.K);
+            for (int b = 0; b < NB; b++) fb[u][b] = row_chunk<T>(pb[b], jin, k, g.K);
 #pragma unroll
-            for (int i = 0; i < FI; i++) fa[u][i] = row_chunk<T, ALIGNED>(pa[i], ain[i], k, g.K);
+            for (int i = 0; i < FI; i++) fa[u][i] = row_chunk<T>(pa[i], ain[i], k, g.K);
         }
 #pragma unroll
         for (int u = 0; u < U; u++)
@@ -722,7 +705,7 @@ __device__ __forceinline__ void chunk_values(u32x4 c, float (&v)[T::chunk]) {
 
 constexpr int kHandful = 4;
 
-template <class T, int M, int EPI, bool ALIGNED>
+template <class T, int M, int EPI>
 __global__ __launch_bounds__(256) void handful_kernel(GemmArgs g, int split) {
     constexpr int NB = EPI == kEpiGated ? 2 : 1;
     __shared__ float part[4][M * NB];
@@ -745,9 +728,9 @@ __global__ __launch_bounds__(256) void handful_kernel(GemmArgs g, int split) {
             for (int u = 0; u < U; u++) {
                 const int64_t k = k0 + u * STEP + lane * T::chunk;
 #pragma unroll
-                for (int b = 0; b < NB; b++) fb[u][b] = row_chunk<T, ALIGNED>(pb + b * up, true, k, g.K);
+                for (int b = 0; b < NB; b++) fb[u][b] = row_chunk<T>(pb + b * up, true, k, g.K);
 #pragma unroll
-                for (int i = 0; i < M; i++) fa[u][i] = row_chunk<T, ALIGNED>(pa + (int64_t)i * g.lda * ES, i < g.I, k, g.K);
+                for (int i = 0; i < M; i++) fa[u][i] = row_chunk<T>(pa + (int64_t)i * g.lda * ES, i < g.I, k, g.K);
             }
 #pragma unroll
             for (int u = 0; u < U; u++) {
@@ -800,41 +783,35 @@ __global__ __launch_bounds__(256) void handful_kernel(GemmArgs g, int split) {
 }
 
 template <class T, int M, int EPI>
-hipError_t launch_handful(bool aligned, const GemmArgs& g, hipStream_t s) {
+hipError_t launch_handful(const GemmArgs& g, hipStream_t s) {
     // waves per column: as many waves as the card holds in one go where columns are few
     const int split = g.J >= 1024 ? 1 : g.J >= 512 ? 2 : 4;
     const dim3 grid((unsigned)((g.J + 4 / split - 1) / (4 / split))), block(256);
-    if (aligned)
-        hipLaunchKernelGGL((handful_kernel<T, M, EPI, true>), grid, block, 0, s, g, split);
-    else
-        hipLaunchKernelGGL((handful_kernel<T, M, EPI, false>), grid, block, 0, s, g, split);
+    hipLaunchKernelGGL((handful_kernel<T, M, EPI>), grid, block, 0, s, g, split);
     return hipGetLastError();
 }
 
 template <class T, int FI, int EPI>
-hipError_t launch_few_one(bool aligned, const GemmArgs& g, hipStream_t s) {
+hipError_t launch_few_one(const GemmArgs& g, hipStream_t s) {
     const dim3 grid((unsigned)((g.J + 15) / 16)), block(kFewWaves * 64);
-    if (aligned)
-        hipLaunchKernelGGL((few_rows_kernel<T, FI, EPI, true>), grid, block, 0, s, g);
-    else
-        hipLaunchKernelGGL((few_rows_kernel<T, FI, EPI, false>), grid, block, 0, s, g);
+    hipLaunchKernelGGL((few_rows_kernel<T, FI, EPI>), grid, block, 0, s, g);
     return hipGetLastError();
 }
 
 template <class T>
-hipError_t launch_few_type(EpiKind kind, bool aligned, const GemmArgs& g, hipStream_t s) {
+hipError_t launch_few_type(EpiKind kind, const GemmArgs& g, hipStream_t s) {
     if (kind == kEpiLinear) {
-        if (g.I == 1) return launch_handful<T, 1, kEpiLinear>(aligned, g, s);
-        if (g.I <= kHandful) return launch_handful<T, kHandful, kEpiLinear>(aligned, g, s);
-        if (g.I <= 16) return launch_few_one<T, 1, kEpiLinear>(aligned, g, s);
-        if (g.I <= 32) return launch_few_one<T, 2, kEpiLinear>(aligned, g, s);
-        if (g.I <= 64) return launch_few_one<T, 4, kEpiLinear>(aligned, g, s);
+        if (g.I == 1) return launch_handful<T, 1, kEpiLinear>(g, s);
+        if (g.I <= kHandful && g.J <= 1024) return launch_handful<T, kHandful, kEpiLinear>(g, s);
+        if (g.I <= 16) return launch_few_one<T, 1, kEpiLinear>(g, s);
+        if (g.I <= 32) return launch_few_one<T, 2, kEpiLinear>(g, s);
+        if (g.I <= 64) return launch_few_one<T, 4, kEpiLinear>(g, s);
     } else if (kind == kEpiGated) {
-        if (g.I == 1) return launch_handful<T, 1, kEpiGated>(aligned, g, s);
-        if (g.I <= kHandful) return launch_handful<T, kHandful, kEpiGated>(aligned, g, s);
-        if (g.I <= 16) return launch_few_one<T, 1, kEpiGated>(aligned, g, s);
-        if (g.I <= 32) return launch_few_one<T, 2, kEpiGated>(aligned, g, s);
-        if (g.I <= 64) return launch_few_one<T, 4, kEpiGated>(aligned, g, s);
+        if (g.I == 1) return launch_handful<T, 1, kEpiGated>(g, s);
+        if (g.I <= kHandful && g.J <= 512) return launch_handful<T, kHandful, kEpiGated>(g, s);
+        if (g.I <= 16) return launch_few_one<T, 1, kEpiGated>(g, s);
+        if (g.I <= 32) return launch_few_one<T, 2, kEpiGated>(g, s);
+        if (g.I <= 64) return launch_few_one<T, 4, kEpiGated>(g, s);
     }
     return hipErrorInvalidValue;
 }

@@ -6,8 +6,8 @@ namespace gsmi {
 hipError_t launch_gemm_bf16(TileShape shape, Layout la, Layout lb, EpiKind kind, const GemmArgs& g, hipStream_t s) {
     return gemm::launch_type<gemm::TBf16>(shape, la, lb, kind, g, s);
 }
-hipError_t launch_few_rows_bf16(EpiKind kind, bool aligned, const GemmArgs& g, hipStream_t s) {
-    return gemm::launch_few_type<gemm::TBf16>(kind, aligned, g, s);
+hipError_t launch_few_rows_bf16(EpiKind kind, const GemmArgs& g, hipStream_t s) {
+    return gemm::launch_few_type<gemm::TBf16>(kind, g, s);
 }
 
 }  // namespace gsmi

@@ -6,8 +6,8 @@ namespace gsmi {
 hipError_t launch_gemm_f16(TileShape shape, Layout la, Layout lb, EpiKind kind, const GemmArgs& g, hipStream_t s) {
     return gemm::launch_type<gemm::TF16>(shape, la, lb, kind, g, s);
 }
-hipError_t launch_few_rows_f16(EpiKind kind, bool aligned, const GemmArgs& g, hipStream_t s) {
-    return gemm::launch_few_type<gemm::TF16>(kind, aligned, g, s);
+hipError_t launch_few_rows_f16(EpiKind kind, const GemmArgs& g, hipStream_t s) {
+    return gemm::launch_few_type<gemm::TF16>(kind, g, s);
 }
 
 }  // namespace gsmi

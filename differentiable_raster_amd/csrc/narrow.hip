@@ -69,6 +69,15 @@ struct Rows {
     }
 };
 
+// Eight values from c on of a row of k; zeros past its end.
+__device__ __forceinline__ u32x4 row_chunk(const uint16_t* row, int32_t c, int32_t k) {
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (c + 8 <= k) return load16(row + c);
+    for (int e = 0; e < 7; e++)
+        if (c + e < k) v[e >> 1] |= (uint32_t)row[c + e] << ((e & 1) * 16);
+    return v;
+}
+
 enum NarrowKind { kPlain = 0, kActivated = 1, kPaired = 2 };
 
 // Workgroups of eight waves that share a CU: two where 128 registers hold the fragments, accumulators and dy.
@@ -116,7 +125,7 @@ __global__ __launch_bounds__(kThreads, 2 * per_cu(KP, NP, KIND)) void narrow_ker
     for (int id = tid; id < NP * (KP / 8); id += kThreads) {
         const int n = id / (KP / 8), c = id % (KP / 8), s = source(n);
         u32x4 v = {0u, 0u, 0u, 0u};
-        if (s >= 0 && c * 8 < a.k) v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.w) + (int64_t)s * a.ldw + c * 8);
+        if (s >= 0) v = row_chunk(static_cast<const uint16_t*>(a.w) + (int64_t)s * a.ldw, c * 8, a.k);
         *reinterpret_cast<u32x4*>(zs + X::at(n, c * 16)) = v;
     }
     __syncthreads();
@@ -161,7 +170,7 @@ __global__ __launch_bounds__(kThreads, 2 * per_cu(KP, NP, KIND)) void narrow_ker
             const int id = tid + n * kThreads, c = id % (KP / 8) * 8;
             const int64_t r = (int64_t)blk * kRows + id / (KP / 8);
             u32x4 v = {0u, 0u, 0u, 0u};
-            if (r < a.rows && c < a.k) v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.x) + r * a.ldx + c);
+            if (r < a.rows) v = row_chunk(static_cast<const uint16_t*>(a.x) + r * a.ldx, c, a.k);
             xr[n] = v;
         }
     };
@@ -172,7 +181,7 @@ __global__ __launch_bounds__(kThreads, 2 * per_cu(KP, NP, KIND)) void narrow_ker
             *reinterpret_cast<u32x4*>(to + X::at(id / (KP / 8), id % (KP / 8) * 16)) = xr[n];
         }
     };
-    const bool vec = a.d_sj == 1 && (a.d_si & 3) == 0 && (H & 3) == 0;
+    const bool vec = a.d_sj == 1 && (H & 3) == 0;
     f32x4 dy[RZ][CZ];
     int64_t dy_lane = ((int64_t)rz0 * 16 + l) * a.d_si + ((int64_t)cz0 * 16 + q * 4) * a.d_sj;
     int64_t dx_lane = ((int64_t)rx0 * 16 + l) * a.ld_dx + kx * 16 + q * 4;
@@ -298,10 +307,11 @@ __global__ __launch_bounds__(kThreads, 2 * per_cu(KP, NP, KIND)) void narrow_ker
             for (int r = 0; r < RX; r++) {
                 if ((int64_t)blk * kRows + (rx0 + r) * 16 + l < a.rows && kx * 16 + q * 4 < a.k) {
                     uint16_t* o = static_cast<uint16_t*>(a.dx) + dx_lane + ((int64_t)blk * kRows + r * 16) * a.ld_dx;
-                    if (a.dx_vec) {
-                        *reinterpret_cast<u32x2*>(o) = u32x2{pack2(acc[r][0], acc[r][1], T::type), pack2(acc[r][2], acc[r][3], T::type)};
+                    if (kx * 16 + q * 4 + 4 <= a.k) {
+                        store_elem4(o, T::type, 0, acc[r]);
                     } else {
-                        for (int k = 0; k < 4; k++) o[k] = (uint16_t)pack2(acc[r][k], 0.0f, T::type);  // a.k is a multiple of 8
+                        for (int k = 0; k < 4; k++)
+                            if (kx * 16 + q * 4 + k < a.k) store_elem(o, T::type, k, acc[r][k]);
                     }
                 }
             }
@@ -364,7 +374,8 @@ __global__ __launch_bounds__(kThreads, 2 * per_cu(KP, NP, KIND)) void narrow_ker
 #pragma unroll
             for (int k = 0; k < KW; k++) {
                 const int j = (kw0 + k) * 16 + q * 4;
-                if (s >= 0 && j < a.k) *reinterpret_cast<f32x4*>(o + (int64_t)s * a.k + j) = dw[n][k];
+                for (int m = 0; m < 4; m++)
+                    if (s >= 0 && j + m < a.k) o[(int64_t)s * a.k + j + m] = dw[n][k][m];
             }
         }
     }

@@ -57,14 +57,14 @@ hipError_t launch_gemm_reduce(const GemmArgs& g, hipStream_t s);
 
 // Products with at most kFewRows rows of a: every row of b is read once, no tile of a.
 constexpr int kFewRows = 64;
-hipError_t launch_few_rows(int type, EpiKind kind, bool aligned, const GemmArgs& g, hipStream_t s);
-hipError_t launch_few_rows_bf16(EpiKind kind, bool aligned, const GemmArgs& g, hipStream_t s);
-hipError_t launch_few_rows_f16(EpiKind kind, bool aligned, const GemmArgs& g, hipStream_t s);
-hipError_t launch_few_rows_e4m3(EpiKind kind, bool aligned, const GemmArgs& g, hipStream_t s);
+hipError_t launch_few_rows(int type, EpiKind kind, const GemmArgs& g, hipStream_t s);
+hipError_t launch_few_rows_bf16(EpiKind kind, const GemmArgs& g, hipStream_t s);
+hipError_t launch_few_rows_f16(EpiKind kind, const GemmArgs& g, hipStream_t s);
+hipError_t launch_few_rows_e4m3(EpiKind kind, const GemmArgs& g, hipStream_t s);
 
 // The backward of a narrow map over many rows in one pass (narrow.hip).
 struct NarrowArgs {
-    const void *x, *w;      // 16-byte aligned rows, k a multiple of 8
+    const void *x, *w;
     int64_t ldx, ldw;
     int32_t rows, k, n;     // n: weight rows (gated: gates, then ups)
     const float* bias;
@@ -74,7 +74,6 @@ struct NarrowArgs {
     int32_t dy_type;
     void* dx;               // optional
     int64_t ld_dx;
-    int32_t dx_vec;         // dx takes 8-byte stores
     float* dw_partial;      // optional: [groups][n][k]
     float* db_partial;      // optional: [db_rows][n]
 };
@@ -85,9 +84,18 @@ struct NarrowShape {
 NarrowShape narrow_shape(int64_t rows, int64_t k, int64_t n, bool gated, bool activated);
 hipError_t launch_narrow(int type, const NarrowArgs& a, bool gated, const NarrowShape& p, hipStream_t s);
 
-// dst[r][c] = src[r * s_row + c * s_col] for c < cols, 0 for c in [cols, ld_dst): an operand in the layout the
-// tiled product reads.  src_type / dst_type: gs_type.  sums (may be null; not for GS_TYPE_E4M3): column sums of
-// the unrounded values per block of rows, [pack_row_blocks(rows)][cols].
+// Copies of operands into the layout that the tiled product reads: dst[r][c] = src[r * s_row + c] for c < cols
+// and 0 for c in [cols, ld); ld a multiple of 16 bytes.  One or two operands in one launch.
+struct PackJob {
+    const void* src;
+    int64_t s_row, rows;
+    int32_t cols;
+    void* dst;
+    int64_t ld;
+};
+hipError_t launch_pack_rows(int from, int to, const PackJob* jobs, int count, hipStream_t s);
+// The same from src[r * s_row + c * s_col], with sums (may be null): column sums of the unrounded values per block
+// of rows, [pack_row_blocks(rows)][cols].  No 8-bit types.
 int64_t pack_row_blocks(int64_t rows);
 hipError_t launch_pack(const void* src, int src_type, int64_t s_row, int64_t s_col, int64_t rows, int32_t cols,
                        void* dst, int dst_type, int64_t ld_dst, float* sums, hipStream_t s);

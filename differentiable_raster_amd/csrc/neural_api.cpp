@@ -165,6 +165,22 @@ gs_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
     return GS_OK;
 }
 
+// x and weight into rows of kp elements where a chunk of 16 bytes does not divide them; null copies are skipped.
+hipError_t copy_operands(const gs_linear_desc* d, Dims& o, const void*& x, const void*& weight, void* x_copy, void* w_copy,
+                         int64_t kp, hipStream_t s) {
+    PackJob jobs[2];
+    int count = 0;
+    if (x_copy) {
+        jobs[count++] = PackJob{x, o.ld_x, o.m, d->in, x_copy, kp};
+        x = x_copy, o.ld_x = kp;
+    }
+    if (w_copy) {
+        jobs[count++] = PackJob{weight, o.ld_w, o.n, d->in, w_copy, kp};
+        weight = w_copy, o.ld_w = kp;
+    }
+    return count ? launch_pack_rows(d->type, d->type, jobs, count, s) : hipSuccess;
+}
+
 gs_status forward(const gs_linear_desc* d, bool gated, const void* x, const float* x_scale, const void* weight,
                   const float* w_scale, const float* bias, const void* residual, void* y, void* ws, size_t ws_bytes,
                   void* stream) {
@@ -205,18 +221,10 @@ gs_status forward(const gs_linear_desc* d, bool gated, const void* x, const floa
         g.e.y_si = cm ? 1 : o.ld_y, g.e.y_sj = cm ? o.ld_y : 1;
         g.e.r_si = cm ? 1 : o.ld_r, g.e.r_sj = cm ? o.ld_r : 1;
         g.e.scale_i = x_scale, g.e.scale_j = w_scale;
-        return launched(launch_few_rows(d->type, kind, !o.pack_x && !o.pack_w, g, s), "product of few rows");
+        return launched(launch_few_rows(d->type, kind, g, s), "product of few rows");
     }
     const int64_t kp = div_up(o.k, o.chunk) * o.chunk;
-    hipError_t e = hipSuccess;
-    if (o.pack_x) {
-        e = launch_pack(x, d->type, o.ld_x, 1, o.m, d->in, f.x, d->type, kp, nullptr, s);
-        x = f.x, o.ld_x = kp;
-    }
-    if (e == hipSuccess && o.pack_w) {
-        e = launch_pack(weight, d->type, o.ld_w, 1, o.n, d->in, f.w, d->type, kp, nullptr, s);
-        weight = f.w, o.ld_w = kp;
-    }
+    hipError_t e = copy_operands(d, o, x, weight, f.x, f.w, kp, s);
     if (e != hipSuccess) return launched(e, "operand copy");
     if (cm) {  // the result's rows are channels: weight is the first operand
         g.a = weight, g.lda = o.ld_w, g.b = x, g.ldb = o.ld_x;
@@ -252,7 +260,7 @@ BackwardPlan plan_backward(const gs_linear_desc* d, const Dims& o, bool gated, v
     std::memset(&p, 0, sizeof(p));
     Carver c{static_cast<char*>(ws)};
     const int es = elem_bytes(d->type);
-    if (!o.pack_x && !o.pack_w) p.narrow = narrow_shape(o.m, o.k, o.n, gated, d->act != GS_ACT_NONE);
+    p.narrow = narrow_shape(o.m, o.k, o.n, gated, d->act != GS_ACT_NONE);
     if (p.narrow.kp) {
         p.partial = c.take((size_t)p.narrow.groups * o.n * o.k * 4);
         p.sums = c.take((size_t)p.narrow.db_rows * o.n * 4);
@@ -305,7 +313,7 @@ gs_status backward(const gs_linear_desc* d, bool gated, const void* x, const voi
         a.rows = d->rows, a.k = d->in, a.n = (int32_t)o.n;
         a.bias = bias, a.act = d->act;
         a.dy = dy, a.dy_type = d->y_type, a.d_si = cm ? 1 : o.ld_y, a.d_sj = cm ? o.ld_y : 1;
-        a.dx = dx, a.ld_dx = o.ld_r, a.dx_vec = o.ld_r % 4 == 0 && reinterpret_cast<uintptr_t>(dx) % 8 == 0;
+        a.dx = dx, a.ld_dx = o.ld_r;
         a.dw_partial = dweight ? static_cast<float*>(p.partial) : nullptr;
         a.db_partial = dbias ? static_cast<float*>(p.sums) : nullptr;
         e = launch_narrow(d->type, a, gated, p.narrow, s);
@@ -320,17 +328,13 @@ gs_status backward(const gs_linear_desc* d, bool gated, const void* x, const voi
             e = launch_colsum(p.sums, GS_TYPE_F32, o.n, p.narrow.db_rows, (int32_t)o.n, static_cast<float*>(p.sums2), dbias, s);
         return launched(e, "backward of a narrow map");
     }
-    if (o.m > 0 && o.pack_x && (p.need_z || dweight)) {
-        e = launch_pack(x, d->type, o.ld_x, 1, o.m, d->in, p.x, d->type, p.kp, nullptr, s);
+    if (o.m > 0) {
+        e = copy_operands(d, o, x, weight, o.pack_x && (p.need_z || dweight) ? p.x : nullptr,
+                          o.pack_w && (p.need_z || dx) ? p.w : nullptr, p.kp, s);
         if (e != hipSuccess) return launched(e, "operand copy");
     }
-    if (o.m > 0 && o.pack_w && (p.need_z || dx)) {
-        e = launch_pack(weight, d->type, o.ld_w, 1, o.n, d->in, p.w, d->type, p.kp, nullptr, s);
-        if (e != hipSuccess) return launched(e, "operand copy");
-    }
-    const void* xo = o.pack_x ? p.x : x;
-    const void* wo = o.pack_w ? p.w : weight;
-    const int64_t ldx = o.pack_x ? p.kp : o.ld_x, ldw = o.pack_w ? p.kp : o.ld_w;
+    const void *xo = x, *wo = weight;
+    const int64_t ldx = o.ld_x, ldw = o.ld_w;
     const int64_t d_si = cm ? 1 : o.ld_y, d_sj = cm ? o.ld_y : 1;
 
     // dz, and the column sums of its unrounded values
@@ -347,8 +351,13 @@ gs_status backward(const gs_linear_desc* d, bool gated, const void* x, const voi
         e = tiled(d->type, p.tz, kRowK, kRowK, gated ? kEpiDGated : kEpiDz, g, s);
         if (e != hipSuccess) return launched(e, "projection of the backward");
     } else if (o.m > 0 && p.need_dz) {
-        e = launch_pack(dy, d->y_type, d_si, d_sj, o.m, (int32_t)o.n, p.dz, d->type, p.np,
-                        dbias ? static_cast<float*>(p.sums) : nullptr, s);
+        if (!cm && !dbias) {
+            const PackJob job{dy, d_si, o.m, (int32_t)o.n, p.dz, p.np};
+            e = launch_pack_rows(d->y_type, d->type, &job, 1, s);
+        } else {
+            e = launch_pack(dy, d->y_type, d_si, d_sj, o.m, (int32_t)o.n, p.dz, d->type, p.np,
+                            dbias ? static_cast<float*>(p.sums) : nullptr, s);
+        }
         if (e != hipSuccess) return launched(e, "gradient copy");
     }
     if (dbias) {

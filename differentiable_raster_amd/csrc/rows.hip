@@ -10,12 +10,6 @@ namespace {
 
 constexpr float kE4m3Max = 448.0f;
 
-// Eight neighbours c..c+7 of a row of `width` values at p, as float32; zeros past the end.
-template <class T>
-__device__ __forceinline__ void load8(const void* base, int64_t at, int32_t c, int32_t width, bool vec, float (&v)[8]);
-template <class T>
-__device__ __forceinline__ void store8(void* base, int64_t at, int32_t c, int32_t width, bool vec, const float (&v)[8]);
-
 struct F32 {
     static constexpr int type = GS_TYPE_F32;
 };
@@ -26,52 +20,25 @@ struct F16 {
     static constexpr int type = GS_TYPE_F16;
 };
 
+// Eight neighbours c..c+7 of a row of `width` values at element `at`, as float32; zeros past the end.
 template <class T>
-__device__ __forceinline__ void load8(const void* base, int64_t at, int32_t c, int32_t width, bool vec, float (&v)[8]) {
-    if (vec) {
-        if (c >= width) {
-            for (int k = 0; k < 8; k++) v[k] = 0.0f;
-        } else if (T::type == GS_TYPE_F32) {
-            const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + at + c);
-            const f32x4 a = p[0], b = p[1];
-            for (int k = 0; k < 4; k++) {
-                v[k] = a[k];
-                v[4 + k] = b[k];
-            }
-        } else {
-            const u32x4 p = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + at + c);
-            for (int k = 0; k < 8; k++) {
-                const uint16_t h = (uint16_t)(p[k >> 1] >> ((k & 1) * 16));
-                v[k] = T::type == GS_TYPE_BF16 ? bf16_to_f32(h) : f16_to_f32(h);
-            }
-        }
+__device__ __forceinline__ void load8(const void* base, int64_t at, int32_t c, int32_t width, float (&v)[8]) {
+    if (c + 8 <= width) {
+        load_elem8(base, T::type, at + c, v);
     } else {
+#pragma unroll
         for (int k = 0; k < 8; k++) v[k] = c + k < width ? load_elem(base, T::type, at + c + k) : 0.0f;
     }
 }
-
 template <class T>
-__device__ __forceinline__ void store8(void* base, int64_t at, int32_t c, int32_t width, bool vec, const float (&v)[8]) {
-    if (vec) {
-        if (c >= width) return;
-        if (T::type == GS_TYPE_F32) {
-            f32x4* p = reinterpret_cast<f32x4*>(static_cast<float*>(base) + at + c);
-            p[0] = f32x4{v[0], v[1], v[2], v[3]};
-            p[1] = f32x4{v[4], v[5], v[6], v[7]};
-        } else {
-            u32x4 p;
-            for (int k = 0; k < 4; k++) p[k] = pack2(v[2 * k], v[2 * k + 1], T::type);
-            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(base) + at + c) = p;
-        }
+__device__ __forceinline__ void store8(void* base, int64_t at, int32_t c, int32_t width, const float (&v)[8]) {
+    if (c + 8 <= width) {
+        store_elem8(base, T::type, at + c, v);
     } else {
+#pragma unroll
         for (int k = 0; k < 8; k++)
             if (c + k < width) store_elem(base, T::type, at + c + k, v[k]);
     }
-}
-
-__device__ __forceinline__ bool vec8(const void* p, int64_t ld, int32_t width, int type) {
-    const int mask = type == GS_TYPE_F32 ? 3 : 7;
-    return (width & 7) == 0 && (ld & mask) == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
 }
 
 // Sum (or maximum of bit patterns) over the NT threads that share a row.
@@ -122,24 +89,21 @@ __global__ __launch_bounds__(block_of(NT)) void norm_fwd_kernel(NormArgs a) {
     const int64_t row = (int64_t)blockIdx.x * rows_per_block(NT) + threadIdx.x / NT;
     const int t = threadIdx.x % NT;
     if (NT <= 64 && row >= a.rows) return;  // NT > 64: one row per block, all of them in range
-    const bool vx = vec8(a.x, a.ld_x, a.width, T::type);
     float v[NC][8];
     float sq = 0.0f;
 #pragma unroll
-    for (int c = 0; c < NC; c++) load8<T>(a.x, row * a.ld_x, (c * NT + t) * 8, a.width, vx, v[c]);
+    for (int c = 0; c < NC; c++) load8<T>(a.x, row * a.ld_x, (c * NT + t) * 8, a.width, v[c]);
     if (a.r) {
-        const bool vr = vec8(a.r, a.ld_r, a.width, T::type);
 #pragma unroll
         for (int c = 0; c < NC; c++) {
             float r[8];
-            load8<T>(a.r, row * a.ld_r, (c * NT + t) * 8, a.width, vr, r);
+            load8<T>(a.r, row * a.ld_r, (c * NT + t) * 8, a.width, r);
             for (int k = 0; k < 8; k++) v[c][k] += r[k];
         }
     }
     if (a.s) {
-        const bool vs = vec8(a.s, a.ld_s, a.width, T::type);
 #pragma unroll
-        for (int c = 0; c < NC; c++) store8<T>(a.s, row * a.ld_s, (c * NT + t) * 8, a.width, vs, v[c]);
+        for (int c = 0; c < NC; c++) store8<T>(a.s, row * a.ld_s, (c * NT + t) * 8, a.width, v[c]);
     }
     if (a.normalize) {
         if (!a.y && !a.q) return;
@@ -151,14 +115,13 @@ __global__ __launch_bounds__(block_of(NT)) void norm_fwd_kernel(NormArgs a) {
 #pragma unroll
         for (int c = 0; c < NC; c++) {
             float w[8];
-            if (a.w) load8<F32>(a.w, 0, (c * NT + t) * 8, a.width, vec8(a.w, 8, a.width, GS_TYPE_F32), w);
+            if (a.w) load8<F32>(a.w, 0, (c * NT + t) * 8, a.width, w);
             for (int k = 0; k < 8; k++) v[c][k] = v[c][k] * rstd * (a.w ? w[k] : 1.0f);
         }
     }
     if (a.y) {
-        const bool vy = vec8(a.y, a.ld_y, a.width, T::type);
 #pragma unroll
-        for (int c = 0; c < NC; c++) store8<T>(a.y, row * a.ld_y, (c * NT + t) * 8, a.width, vy, v[c]);
+        for (int c = 0; c < NC; c++) store8<T>(a.y, row * a.ld_y, (c * NT + t) * 8, a.width, v[c]);
     }
     if (a.q) {
         // the largest magnitude by its bit pattern: a NaN's is larger than every number's
@@ -174,7 +137,6 @@ __global__ __launch_bounds__(block_of(NT)) void norm_fwd_kernel(NormArgs a) {
         const bool zero = amax < 1e-30f;
         if (t == 0) a.q_scale[row] = zero ? 0.0f : amax / kE4m3Max;
         const float inv = zero ? 0.0f : kE4m3Max / amax;
-        const bool vq = (a.width & 7) == 0 && (a.ld_y & 7) == 0 && (reinterpret_cast<uintptr_t>(a.q) & 7) == 0;
 #pragma unroll
         for (int c = 0; c < NC; c++) {
             const int32_t col = (c * NT + t) * 8;
@@ -185,8 +147,9 @@ __global__ __launch_bounds__(block_of(NT)) void norm_fwd_kernel(NormArgs a) {
             lo = __builtin_amdgcn_cvt_pk_fp8_f32(o[2], o[3], lo, true);
             hi = __builtin_amdgcn_cvt_pk_fp8_f32(o[6], o[7], hi, true);
             uint8_t* p = a.q + row * a.ld_y + col;
-            if (vq) {
-                *reinterpret_cast<u32x2*>(p) = u32x2{(uint32_t)lo, (uint32_t)hi};
+            if (col + 8 <= a.width) {
+                const u32x2 both = {(uint32_t)lo, (uint32_t)hi};
+                __builtin_memcpy(p, &both, 8);
             } else {
                 for (int k = 0; k < 8; k++)
                     if (col + k < a.width) p[k] = (uint8_t)((uint32_t)(k < 4 ? lo : hi) >> ((k & 3) * 8));
@@ -204,12 +167,10 @@ __global__ __launch_bounds__(block_of(NT)) void norm_bwd_kernel(NormArgs a) {
     __shared__ float shares[RPB > 1 ? RPB * WIDTH : 1];
     const int64_t group = (int64_t)blockIdx.x * RPB + threadIdx.x / NT, groups = (int64_t)gridDim.x * RPB;
     const int t = threadIdx.x % NT;
-    const bool vs = vec8(a.s, a.ld_s, a.width, T::type), vy = vec8(a.dy, a.ld_y, a.width, T::type);
-    const bool vr = vec8(a.ds, a.ld_r, a.width, T::type), vx = vec8(a.dx, a.ld_x, a.width, T::type);
     float w[NC][8], acc[NC][8];
 #pragma unroll
     for (int c = 0; c < NC; c++) {
-        if (a.w) load8<F32>(a.w, 0, (c * NT + t) * 8, a.width, vec8(a.w, 8, a.width, GS_TYPE_F32), w[c]);
+        if (a.w) load8<F32>(a.w, 0, (c * NT + t) * 8, a.width, w[c]);
         for (int k = 0; k < 8; k++) {
             if (!a.w) w[c][k] = 1.0f;
             acc[c][k] = 0.0f;
@@ -219,9 +180,9 @@ __global__ __launch_bounds__(block_of(NT)) void norm_bwd_kernel(NormArgs a) {
         float s[NC][8], g[NC][8], d[NC][8];
 #pragma unroll
         for (int c = 0; c < NC; c++) {
-            load8<T>(a.s, row * a.ld_s, (c * NT + t) * 8, a.width, vs, s[c]);
-            load8<T>(a.dy, row * a.ld_y, (c * NT + t) * 8, a.width, vy, g[c]);
-            if (a.ds) load8<T>(a.ds, row * a.ld_r, (c * NT + t) * 8, a.width, vr, d[c]);
+            load8<T>(a.s, row * a.ld_s, (c * NT + t) * 8, a.width, s[c]);
+            load8<T>(a.dy, row * a.ld_y, (c * NT + t) * 8, a.width, g[c]);
+            if (a.ds) load8<T>(a.ds, row * a.ld_r, (c * NT + t) * 8, a.width, d[c]);
         }
         float sq = 0.0f, dot = 0.0f;
 #pragma unroll
@@ -240,14 +201,14 @@ __global__ __launch_bounds__(block_of(NT)) void norm_bwd_kernel(NormArgs a) {
                 const float o = rstd * fmaf(-n, mean, g[c][k] * w[c][k]);
                 g[c][k] = a.ds ? d[c][k] + o : o;
             }
-            store8<T>(a.dx, row * a.ld_x, (c * NT + t) * 8, a.width, vx, g[c]);
+            store8<T>(a.dx, row * a.ld_x, (c * NT + t) * 8, a.width, g[c]);
         }
     }
     if (!a.partial) return;
     if (RPB == 1) {
 #pragma unroll
         for (int c = 0; c < NC; c++)
-            store8<F32>(a.partial, (int64_t)blockIdx.x * a.width, (c * NT + t) * 8, a.width, (a.width & 7) == 0, acc[c]);
+            store8<F32>(a.partial, (int64_t)blockIdx.x * a.width, (c * NT + t) * 8, a.width, acc[c]);
         return;
     }
 #pragma unroll
@@ -353,11 +314,42 @@ __global__ __launch_bounds__(256) void pack_kernel(const void* src, int src_type
     __syncthreads();
     if (y == 0 && c0 + x < cols) sums[(int64_t)blockIdx.x * cols + c0 + x] = (part[0][x] + part[1][x]) + (part[2][x] + part[3][x]);
 }
-// The same for bytes (8-bit operands), rows contiguous on both sides.
-__global__ __launch_bounds__(256) void pack_bytes_kernel(const uint8_t* src, int64_t s_row, int64_t rows, int32_t cols,
-                                                         uint8_t* dst, int64_t ld) {
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        for (int64_t c = threadIdx.x; c < ld; c += 256) dst[r * ld + c] = c < cols ? src[r * s_row + c] : (uint8_t)0;
+// Rows along memory on both sides, of up to two operands in one launch: a thread writes one 16-byte chunk.
+struct PackJobs {
+    PackJob j[2];
+};
+template <int FROM, int TO>
+__device__ __forceinline__ u32x4 packed_chunk(const PackJob& p, int64_t r, int32_t c) {
+    if (TO == GS_TYPE_E4M3) {
+        const uint8_t* s = static_cast<const uint8_t*>(p.src) + r * p.s_row + c;
+        if (c + 16 <= p.cols) return load16(s);
+        u32x4 v = {0u, 0u, 0u, 0u};
+        for (int k = 0; k < 16; k++)
+            if (c + k < p.cols) v[k >> 2] |= (uint32_t)s[k] << ((k & 3) * 8);
+        return v;
+    }
+    float v[8];
+    const int64_t at = r * p.s_row;
+    if (FROM == TO && c + 8 <= p.cols) return load16(static_cast<const uint16_t*>(p.src) + at + c);
+    if (c + 8 <= p.cols) {
+        load_elem8(p.src, FROM, at + c, v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; k++) v[k] = c + k < p.cols ? load_elem(p.src, FROM, at + c + k) : 0.0f;
+    }
+    return u32x4{pack2(v[0], v[1], TO), pack2(v[2], v[3], TO), pack2(v[4], v[5], TO), pack2(v[6], v[7], TO)};
+}
+template <int FROM, int TO>
+__global__ __launch_bounds__(256) void pack_rows_kernel(PackJobs jobs) {
+    const PackJob p = jobs.j[blockIdx.y];
+    constexpr int CHUNK = TO == GS_TYPE_E4M3 ? 16 : 8;
+    const int32_t per_row = (int32_t)(p.ld / CHUNK);
+    const int64_t total = p.rows * per_row;
+    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < total; n += (int64_t)gridDim.x * 256) {
+        const int64_t row = n / per_row;
+        const int32_t c = (int32_t)(n - row * per_row);
+        static_cast<u32x4*>(p.dst)[n] = packed_chunk<FROM, TO>(p, row, c * CHUNK);
+    }
 }
 
 // ---- column sums ----------------------------------------------------------------------------------
@@ -365,7 +357,7 @@ __global__ __launch_bounds__(256) void pack_bytes_kernel(const uint8_t* src, int
 // 32 sums meet in LDS in a fixed order.
 template <class T>
 __global__ __launch_bounds__(256) void colsum_kernel(const void* in, int64_t s_row, int64_t rows, int32_t cols,
-                                                     int64_t rows_per_part, bool vec, float* out) {
+                                                     int64_t rows_per_part, float* out) {
     __shared__ float part[32][65];
     const int x = (threadIdx.x & 7) * 8, y = threadIdx.x >> 3;
     const int32_t c = blockIdx.x * 64 + x;
@@ -375,7 +367,7 @@ __global__ __launch_bounds__(256) void colsum_kernel(const void* in, int64_t s_r
 #pragma unroll 4
         for (int64_t r = r0 + y; r < r1; r += 32) {
             float v[8];
-            load8<T>(in, r * s_row, c, cols, vec, v);
+            load8<T>(in, r * s_row, c, cols, v);
             for (int k = 0; k < 8; k++) s[k] += v[k];
         }
     for (int k = 0; k < 8; k++) part[y][x + k] = s[k];
@@ -399,13 +391,12 @@ int64_t colsum_parts(int64_t rows, int32_t cols) {
 hipError_t launch_colsum_stage(const void* in, int type, int64_t s_row, int64_t rows, int32_t cols, int64_t parts, int64_t per,
                                float* out, hipStream_t s) {
     const dim3 grid((unsigned)((cols + 63) / 64), (unsigned)parts);
-    const bool vec = (cols & 7) == 0 && (s_row & 7) == 0 && (reinterpret_cast<uintptr_t>(in) & 15) == 0;
     if (type == GS_TYPE_F32)
-        hipLaunchKernelGGL(colsum_kernel<F32>, grid, dim3(256), 0, s, in, s_row, rows, cols, per, vec, out);
+        hipLaunchKernelGGL(colsum_kernel<F32>, grid, dim3(256), 0, s, in, s_row, rows, cols, per, out);
     else if (type == GS_TYPE_BF16)
-        hipLaunchKernelGGL(colsum_kernel<Bf16>, grid, dim3(256), 0, s, in, s_row, rows, cols, per, vec, out);
+        hipLaunchKernelGGL(colsum_kernel<Bf16>, grid, dim3(256), 0, s, in, s_row, rows, cols, per, out);
     else
-        hipLaunchKernelGGL(colsum_kernel<F16>, grid, dim3(256), 0, s, in, s_row, rows, cols, per, vec, out);
+        hipLaunchKernelGGL(colsum_kernel<F16>, grid, dim3(256), 0, s, in, s_row, rows, cols, per, out);
     return hipGetLastError();
 }
 
@@ -478,17 +469,38 @@ hipError_t launch_norm_bwd(int type, const NormArgs& a, hipStream_t s) {
 
 int64_t pack_row_blocks(int64_t rows) { return (rows + 63) / 64; }
 
+hipError_t launch_pack_rows(int from, int to, const PackJob* jobs, int count, hipStream_t s) {
+    PackJobs a;
+    int64_t most = 0;
+    for (int k = 0; k < 2; k++) {
+        a.j[k] = jobs[k < count ? k : 0];
+        const int64_t total = a.j[k].rows * (a.j[k].ld / (to == GS_TYPE_E4M3 ? 16 : 8));
+        if (total > most) most = total;
+    }
+    if (count < 1 || most == 0) return hipSuccess;
+    int64_t blocks = (most + 255) / 256;
+    if (blocks > 8192) blocks = 8192;
+    const dim3 grid((unsigned)blocks, (unsigned)count);
+    if (to == GS_TYPE_E4M3)
+        hipLaunchKernelGGL((pack_rows_kernel<GS_TYPE_E4M3, GS_TYPE_E4M3>), grid, dim3(256), 0, s, a);
+    else if (from == to)  // bits as they are
+        hipLaunchKernelGGL((pack_rows_kernel<GS_TYPE_BF16, GS_TYPE_BF16>), grid, dim3(256), 0, s, a);
+    else if (from == GS_TYPE_F32 && to == GS_TYPE_BF16)
+        hipLaunchKernelGGL((pack_rows_kernel<GS_TYPE_F32, GS_TYPE_BF16>), grid, dim3(256), 0, s, a);
+    else if (from == GS_TYPE_F32)
+        hipLaunchKernelGGL((pack_rows_kernel<GS_TYPE_F32, GS_TYPE_F16>), grid, dim3(256), 0, s, a);
+    else if (to == GS_TYPE_BF16)
+        hipLaunchKernelGGL((pack_rows_kernel<GS_TYPE_F16, GS_TYPE_BF16>), grid, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((pack_rows_kernel<GS_TYPE_BF16, GS_TYPE_F16>), grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
 hipError_t launch_pack(const void* src, int src_type, int64_t s_row, int64_t s_col, int64_t rows, int32_t cols, void* dst,
                        int dst_type, int64_t ld_dst, float* sums, hipStream_t s) {
     if (rows <= 0) return hipSuccess;
-    if (src_type == GS_TYPE_E4M3) {
-        const unsigned blocks = (unsigned)(rows < 65536 ? rows : 65536);
-        hipLaunchKernelGGL(pack_bytes_kernel, dim3(blocks), dim3(256), 0, s, static_cast<const uint8_t*>(src), s_row, rows,
-                           cols, static_cast<uint8_t*>(dst), ld_dst);
-    } else {
-        hipLaunchKernelGGL(pack_kernel, dim3((unsigned)((rows + 63) / 64), (unsigned)((ld_dst + 63) / 64)), dim3(256), 0, s,
-                           src, src_type, s_row, s_col, rows, cols, dst, dst_type, ld_dst, sums);
-    }
+    hipLaunchKernelGGL(pack_kernel, dim3((unsigned)((rows + 63) / 64), (unsigned)((ld_dst + 63) / 64)), dim3(256), 0, s, src,
+                       src_type, s_row, s_col, rows, cols, dst, dst_type, ld_dst, sums);
     return hipGetLastError();
 }
 
@@ -519,10 +531,10 @@ hipError_t launch_gemm(int type, TileShape shape, Layout la, Layout lb, EpiKind 
     return launch_gemm_e4m3(shape, la, lb, kind, g, s);
 }
 
-hipError_t launch_few_rows(int type, EpiKind kind, bool aligned, const GemmArgs& g, hipStream_t s) {
-    if (type == GS_TYPE_BF16) return launch_few_rows_bf16(kind, aligned, g, s);
-    if (type == GS_TYPE_F16) return launch_few_rows_f16(kind, aligned, g, s);
-    return launch_few_rows_e4m3(kind, aligned, g, s);
+hipError_t launch_few_rows(int type, EpiKind kind, const GemmArgs& g, hipStream_t s) {
+    if (type == GS_TYPE_BF16) return launch_few_rows_bf16(kind, g, s);
+    if (type == GS_TYPE_F16) return launch_few_rows_f16(kind, g, s);
+    return launch_few_rows_e4m3(kind, g, s);
 }
 
 hipError_t launch_gemm_reduce(const GemmArgs& g, hipStream_t s) {
