@@ -257,21 +257,60 @@ struct Operand {
             }
         }
     }
-    // p: first element of the tile's free rows at k = 0; rows: free rows from there to the operand's end
-    // (kRowK: at most what the tile reads; kRowFree: columns); left: k from the step's first to the end.
-    __device__ __forceinline__ void load(char* tile, int wave, const char* p, int64_t ld, int64_t k0, int32_t rows, int64_t left) const {
-        const bool whole = left >= BK;
-        const int32_t l = whole ? BK : (int32_t)left;
-        const char* base = LAYOUT == kRowK ? p + k0 * ES : p + k0 * ld * ES;
-        // a row along k ends with whole chunks: the operand is padded with zeros where k does not
-        const int32_t lp = (l + T::chunk - 1) / T::chunk * T::chunk;
-        const int32_t bytes = LAYOUT == kRowK ? (int32_t)(((int64_t)(rows - 1) * ld + lp) * ES)
-                                              : (int32_t)(((int64_t)(l - 1) * ld + rows) * ES);
-        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, bytes, 0x00020000);
+    const char* next;    // first byte of the next step's rows (kRowK: of the tile's free rows; kRowFree: of its k rows)
+    int64_t stride;      // bytes from one step to the next
+    int32_t whole;       // bytes that a whole step's chunks may touch from there on
+    int32_t rows_bytes;  // kRowK: bytes of all rows but the last; kRowFree: of one row's columns in reach
+
+    // p: first element of the tile's free rows at k = 0; k: the first step's; rows: free rows from p to the
+    // operand's end (kRowK: at most what the tile reads; kRowFree: columns)
+    __device__ __forceinline__ void start(const char* p, int64_t ld, int64_t k, int32_t rows) {
+        if (LAYOUT == kRowK) {
+            next = p + k * ES;
+            stride = kStepBytes;
+            rows_bytes = (int32_t)((rows - 1) * ld * ES);
+            whole = rows_bytes + kStepBytes;
+        } else {
+            next = p + k * ld * ES;
+            stride = BK * ld * ES;
+            rows_bytes = rows * ES;
+            whole = (int32_t)((BK - 1) * ld * ES) + rows_bytes;
+        }
+    }
+    __device__ __forceinline__ void issue(char* tile, int wave, int32_t bytes, int32_t reach) {
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(next), 0, bytes, 0x00020000);
 #pragma unroll
         for (int n = 0; n < N; n++)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(tile + n * THREADS * 16 + wave * 1024), 16,
-                                                     whole || first_k + n * KPN < l ? off[n] : kOutside, 0, 0, 0);
+                                                     first_k + n * KPN < reach ? off[n] : kOutside, 0, 0, 0);
+        next += stride;
+    }
+    // the same into registers, which put() takes to where the other would
+    __device__ __forceinline__ void issue(u32x4 (&to)[N], int32_t bytes, int32_t reach) {
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(next), 0, bytes, 0x00020000);
+#pragma unroll
+        for (int n = 0; n < N; n++)
+            to[n] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, first_k + n * KPN < reach ? off[n] : kOutside, 0, 0));
+        next += stride;
+    }
+    __device__ __forceinline__ void put(char* tile, int tid, const u32x4 (&from)[N]) const {
+#pragma unroll
+        for (int n = 0; n < N; n++) *reinterpret_cast<u32x4*>(tile + (n * THREADS + tid) * 16) = from[n];
+    }
+    __device__ __forceinline__ void load(u32x4 (&to)[N], int64_t ld, int64_t left) {
+        const int32_t l = left < BK ? (int32_t)left : BK, lp = (l + T::chunk - 1) / T::chunk * T::chunk;
+        issue(to, LAYOUT == kRowK ? rows_bytes + lp * ES : (int32_t)((l - 1) * ld * ES) + rows_bytes, l);
+    }
+    // left: k from the step's first to the end; all of BK (the usual case) asks for no comparison
+    __device__ __forceinline__ void load(char* tile, int wave, int64_t ld, int64_t left) {
+        if (left >= BK) {
+            issue(tile, wave, whole, 0x7FFFFFFF);
+        } else {
+            const int32_t l = (int32_t)left;
+            // a row along k ends with whole chunks: the operand is padded with zeros where k does not
+            const int32_t lp = (l + T::chunk - 1) / T::chunk * T::chunk;
+            issue(tile, wave, LAYOUT == kRowK ? rows_bytes + lp * ES : (int32_t)((l - 1) * ld * ES) + rows_bytes, l);
+        }
     }
 };
 
@@ -328,7 +367,7 @@ __device__ __forceinline__ void tile_of(int32_t id, int32_t ni, int32_t nj, int3
 }
 
 template <class T, int SHAPE, int LA, int LB, int EPI>
-__global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(GemmArgs g) {
+__global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256, 2) void gemm_kernel(GemmArgs g) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host needs the kernel's name alone
     constexpr int BI = kTileDims[SHAPE].bi, BJ = kTileDims[SHAPE].bj, WI = kTileDims[SHAPE].wi;
     constexpr int THREADS = SHAPE == kTile256 ? 512 : 256, WJ = THREADS / 64 / WI;
@@ -369,38 +408,14 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
 #pragma unroll
         for (int j = 0; j < FJ; j++) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    constexpr bool WHOLE = T::chunk == 16;  // a product takes the whole step of its rows
-    constexpr int PARTS = WHOLE && FI >= 4 ? 4 : 2, H = FI / PARTS;  // blocks of a whose fragments are held together
     Reader<BI, LA> reada;
     Reader<BJ, LB> readb;
     reada.init(wi * FI, lane);
     readb.init(wj * FJ, lane);
-    u32x4 fa[2][WHOLE ? 2 * H : H], fb[2][FJ];
     auto fetch = [&](char* ta, char* tb, int32_t kt) {
-        const int64_t k = (int64_t)kt * BK;
-        oa.load(ta, wave, pa, g.lda, k, ra, g.K - k);
-        ob.load(tb, wave, pb, g.ldb, k, rb, g.K - k);
-    };
-    auto read_a = [&](const char* ta, int kk, int part) {
-#pragma unroll
-        for (int i = 0; i < H; i++) fa[part & 1][WHOLE ? kk * H + i : i] = reada.read(ta, part * H + i, kk);
-    };
-    auto read_b = [&](const char* tb, int kk) {
-#pragma unroll
-        for (int j = 0; j < FJ; j++) fb[kk][j] = readb.read(tb, j, kk);
-    };
-    auto multiply = [&](int kk, int part) {
-#pragma unroll
-        for (int i = 0; i < H; i++)
-#pragma unroll
-            for (int j = 0; j < FJ; j++) {
-                f32x4& sum = acc[part * H + i][j];
-                if constexpr (WHOLE)
-                    sum = T::mma2(fb[0][j], fb[1][j], fa[part & 1][i], fa[part & 1][H + i], sum);
-                else
-                    sum = T::mma(fb[kk][j], fa[part][i], sum);
-            }
-        __builtin_amdgcn_sched_barrier(0);
+        const int64_t left = g.K - (int64_t)kt * BK;
+        oa.load(ta, wave, g.lda, left);
+        ob.load(tb, wave, g.ldb, left);
     };
     // Every load from memory to LDS has landed, and every wave is here.  The barrier alone would not wait for
     // the loads.
@@ -408,56 +423,166 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256) void gemm_kernel(Gem
         __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
         __syncthreads();
     };
-    // A step works on one tile while the other is filled, in quarters: the fragments of a quarter are read
-    // before the products of the one before it, so that LDS latency hides behind products.  Once every wave
-    // has read its last fragments the tile is free for step kt + 2.
-    auto step = [&](char* ta, char* tb, char* next_a, char* next_b, int32_t kt) {
-        reada.renew();
-        readb.renew();
-        if constexpr (WHOLE) {
+    oa.start(pa, g.lda, (int64_t)kt0 * BK, ra);
+    ob.start(pb, g.ldb, (int64_t)kt0 * BK, rb);
+    if (SHAPE != kTile64Far) {
+        if (kt0 < kt1) fetch(a0, b0, kt0);
+        if (kt0 + 1 < kt1) fetch(a1, b1, kt0 + 1);
+        landed();
+    }
+    if constexpr (SHAPE == kTile64Far) {
+        // For few tiles and many steps, where a step of the other form lasts as long as its loads (0.5 us).  The
+        // chunks pass through registers, four steps ahead; the compiler waits for a load to LDS together with all
+        // later ones, so that form cannot be that far ahead.  128 x 4096 x 4096: 33.8 -> 23.6 us; with four tiles
+        // to a CU it loses (2048^3: 28 -> 34 us), because fewer fit.
+        u32x4 ra4[4][OpA::N], rb4[4][OpB::N];
+        auto get = [&](auto set, int32_t kt) {
+            constexpr int s = decltype(set)::value;
+            if (kt >= kt1) return;
+            const int64_t left = g.K - (int64_t)kt * BK;
+            oa.load(ra4[s], g.lda, left);
+            ob.load(rb4[s], g.ldb, left);
+        };
+        auto step = [&](const char* ta, const char* tb, char* next_a, char* next_b, int32_t kt, auto set) {
+            constexpr int s = decltype(set)::value;  // registers of tile kt + 1
+            u32x4 fa[2][FI], fb[2][FJ];
 #pragma unroll
-            for (int p = 0; p + 1 < PARTS; p++) {
-                read_a(ta, 0, p + 1);
-                read_a(ta, 1, p + 1);
-                multiply(0, p);
+            for (int kk = 0; kk < 2; kk++) {
+#pragma unroll
+                for (int j = 0; j < FJ; j++) fb[kk][j] = readb.read(tb, j, kk);
+#pragma unroll
+                for (int i = 0; i < FI; i++) fa[kk][i] = reada.read(ta, i, kk);
             }
+            if (kt + 1 < kt1) {
+                oa.put(next_a, tid, ra4[s]);
+                ob.put(next_b, tid, rb4[s]);
+                get(set, kt + 5);
+            }
+#pragma unroll
+            for (int i = 0; i < FI; i++)
+#pragma unroll
+                for (int j = 0; j < FJ; j++) {
+                    if constexpr (T::chunk == 16) {
+                        acc[i][j] = T::mma2(fb[0][j], fb[1][j], fa[0][i], fa[1][i], acc[i][j]);
+                    } else {
+                        acc[i][j] = T::mma(fb[0][j], fa[0][i], acc[i][j]);
+                        acc[i][j] = T::mma(fb[1][j], fa[1][i], acc[i][j]);
+                    }
+                }
+            __syncthreads();
+        };
+        typedef std::integral_constant<int, 0> S0;
+        typedef std::integral_constant<int, 1> S1;
+        typedef std::integral_constant<int, 2> S2;
+        typedef std::integral_constant<int, 3> S3;
+        get(S0(), kt0);
+        get(S1(), kt0 + 1);
+        get(S2(), kt0 + 2);
+        get(S3(), kt0 + 3);
+        if (kt0 < kt1) {
+            oa.put(a0, tid, ra4[0]);
+            ob.put(b0, tid, rb4[0]);
+            get(S0(), kt0 + 4);
+        }
+        __syncthreads();
+        int32_t kt = kt0;
+        for (; kt + 4 <= kt1; kt += 4) {
+            step(a0, b0, a1, b1, kt, S1());
+            step(a1, b1, a0, b0, kt + 1, S2());
+            step(a0, b0, a1, b1, kt + 2, S3());
+            step(a1, b1, a0, b0, kt + 3, S0());
+        }
+        if (kt < kt1) step(a0, b0, a1, b1, kt, S1());
+        if (kt + 1 < kt1) step(a1, b1, a0, b0, kt + 1, S2());
+        if (kt + 2 < kt1) step(a0, b0, a1, b1, kt + 2, S3());
+    } else if constexpr (SHAPE == kTile256) {
+        // A step works on one tile while the other is filled, in quarters: the fragments of a quarter are read
+        // before the products of the one before it, so that LDS latency hides behind products.  Once every wave
+        // has read its last fragments the tile is free for step kt + 2.
+        constexpr int H = FI / 2;
+        u32x4 fa[2][H], fb[2][FJ];
+        auto read_a = [&](const char* ta, int kk, int half) {
+#pragma unroll
+            for (int i = 0; i < H; i++) fa[half][i] = reada.read(ta, half * H + i, kk);
+        };
+        auto read_b = [&](const char* tb, int kk) {
+#pragma unroll
+            for (int j = 0; j < FJ; j++) fb[kk][j] = readb.read(tb, j, kk);
+        };
+        auto multiply = [&](int kk, int half) {
+#pragma unroll
+            for (int i = 0; i < H; i++)
+#pragma unroll
+                for (int j = 0; j < FJ; j++) acc[half * H + i][j] = T::mma(fb[kk][j], fa[half][i], acc[half * H + i][j]);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto step = [&](char* ta, char* tb, char* next_a, char* next_b, int32_t kt) {
+            reada.renew();
+            readb.renew();
+            read_a(ta, 0, 1);
+            multiply(0, 0);
+            read_a(ta, 1, 0);
+            read_b(tb, 1);
+            multiply(0, 1);
+            read_a(ta, 1, 1);
+            multiply(1, 0);
             landed();
             if (kt + 2 < kt1) fetch(ta, tb, kt + 2);
-            read_a(next_a, 0, 0);
-            read_a(next_a, 1, 0);
-            multiply(0, PARTS - 1);
+            read_a(next_a, 0, 0);  // after the last step: values that no product takes
             read_b(next_b, 0);
-            read_b(next_b, 1);
-            return;
+            multiply(1, 1);
+        };
+        read_a(a0, 0, 0);
+        read_b(b0, 0);
+        int32_t kt = kt0;
+        for (; kt + 2 <= kt1; kt += 2) {
+            step(a0, b0, a1, b1, kt);
+            step(a1, b1, a0, b0, kt + 1);
         }
-        read_a(ta, 0, 1);
-        multiply(0, 0);
-        read_a(ta, 1, 0);
-        read_b(tb, 1);
-        multiply(0, 1);
-        read_a(ta, 1, 1);
-        multiply(1, 0);
-        landed();
-        if (kt + 2 < kt1) fetch(ta, tb, kt + 2);
-        read_a(next_a, 0, 0);  // after the last step: values that no product takes
-        read_b(next_b, 0);
-        multiply(1, 1);
-    };
-    if (kt0 < kt1) fetch(a0, b0, kt0);
-    if (kt0 + 1 < kt1) fetch(a1, b1, kt0 + 1);
-    landed();
-    read_a(a0, 0, 0);
-    read_b(b0, 0);
-    if constexpr (WHOLE) {
-        read_a(a0, 1, 0);
-        read_b(b0, 1);
+        if (kt < kt1) step(a0, b0, a1, b1, kt);
+    } else {
+        // The fragments of a whole step fit the registers twice: a step's products run while the next step's
+        // fragments are read and the tile after it is filled.  A step of a small tile has few products, so its
+        // time is one latency of LDS and a barrier, not one for each part.
+        u32x4 fa[2][2][FI], fb[2][2][FJ];
+        auto read = [&](const char* ta, const char* tb, auto set) {
+            constexpr int p = decltype(set)::value;
+#pragma unroll
+            for (int kk = 0; kk < 2; kk++) {
+#pragma unroll
+                for (int j = 0; j < FJ; j++) fb[p][kk][j] = readb.read(tb, j, kk);
+#pragma unroll
+                for (int i = 0; i < FI; i++) fa[p][kk][i] = reada.read(ta, i, kk);
+            }
+        };
+        auto step = [&](char* ta, char* tb, char* next_a, char* next_b, int32_t kt, auto set) {
+            constexpr int p = decltype(set)::value;
+            landed();
+            if (kt + 2 < kt1) fetch(ta, tb, kt + 2);
+            read(next_a, next_b, std::integral_constant<int, 1 - p>());  // after the last step: values that no product takes
+#pragma unroll
+            for (int i = 0; i < FI; i++)
+#pragma unroll
+                for (int j = 0; j < FJ; j++) {
+                    if constexpr (T::chunk == 16) {
+                        acc[i][j] = T::mma2(fb[p][0][j], fb[p][1][j], fa[p][0][i], fa[p][1][i], acc[i][j]);
+                    } else {
+                        acc[i][j] = T::mma(fb[p][0][j], fa[p][0][i], acc[i][j]);
+                        acc[i][j] = T::mma(fb[p][1][j], fa[p][1][i], acc[i][j]);
+                    }
+                }
+        };
+        typedef std::integral_constant<int, 0> Even;
+        typedef std::integral_constant<int, 1> Odd;
+        read(a0, b0, Even());
+        int32_t kt = kt0;
+        for (; kt + 2 <= kt1; kt += 2) {
+            step(a0, b0, a1, b1, kt, Even());
+            step(a1, b1, a0, b0, kt + 1, Odd());
+        }
+        if (kt < kt1) step(a0, b0, a1, b1, kt, Even());
+        __syncthreads();  // the last tile's memory takes the sums
     }
-    int32_t kt = kt0;
-    for (; kt + 2 <= kt1; kt += 2) {
-        step(a0, b0, a1, b1, kt);
-        step(a1, b1, a0, b0, kt + 1);
-    }
-    if (kt < kt1) step(a0, b0, a1, b1, kt);
 
     // The sums go through LDS, a wave's rows at a time, so that a lane ends with eight neighbours of a row:
     // results, residuals and gradients move in whole lines, and the epilogue's code stands here once.
@@ -597,6 +722,7 @@ hipError_t launch_type(TileShape shape, Layout la, Layout lb, EpiKind kind, cons
         case kTile64: return launch_shape<T, kTile64>(la, lb, kind, g, s);
         case kTile64x256: return launch_shape<T, kTile64x256>(la, lb, kind, g, s);
         case kTile256x64: return launch_shape<T, kTile256x64>(la, lb, kind, g, s);
+        case kTile64Far: return launch_shape<T, kTile64Far>(la, lb, kind, g, s);
         default: return hipErrorInvalidValue;
     }
 }

@@ -374,8 +374,13 @@ __global__ __launch_bounds__(kThreads, 2 * per_cu(KP, NP, KIND)) void narrow_ker
 #pragma unroll
             for (int k = 0; k < KW; k++) {
                 const int j = (kw0 + k) * 16 + q * 4;
-                for (int m = 0; m < 4; m++)
-                    if (s >= 0 && j + m < a.k) o[(int64_t)s * a.k + j + m] = dw[n][k][m];
+                if (s < 0) continue;
+                if (j + 4 <= a.k) {
+                    store_elem4(o, GS_TYPE_F32, (int64_t)s * a.k + j, dw[n][k]);
+                } else {
+                    for (int m = 0; m < 4; m++)
+                        if (j + m < a.k) o[(int64_t)s * a.k + j + m] = dw[n][k][m];
+                }
             }
         }
     }

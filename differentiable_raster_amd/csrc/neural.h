@@ -40,12 +40,12 @@ struct GemmArgs {
     Epi e;
 };
 
-// Tile shapes of the tiled product.
-enum TileShape { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile64x256 = 3, kTile256x64 = 4, kTileShapes = 5 };
+// Tile shapes of the tiled product; kTile64Far loads its tiles four steps ahead.
+enum TileShape { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile64x256 = 3, kTile256x64 = 4, kTile64Far = 5, kTileShapes = 6 };
 struct TileDims {
     int bi, bj, wi;  // rows, columns (of b) and i-strips (waves along i) of a tile
 };
-constexpr TileDims kTileDims[kTileShapes] = {{256, 256, 2}, {128, 128, 2}, {64, 64, 2}, {64, 256, 1}, {256, 64, 4}};
+constexpr TileDims kTileDims[kTileShapes] = {{256, 256, 2}, {128, 128, 2}, {64, 64, 2}, {64, 256, 1}, {256, 64, 4}, {64, 64, 2}};
 constexpr int kStepBytes = 128;  // bytes of one row that a step of the summed axis takes
 
 // type: gs_type of both operands (BF16, F16, E4M3).  E4M3: only a, b with kRowK and the forward kinds.

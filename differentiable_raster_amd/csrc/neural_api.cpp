@@ -52,16 +52,16 @@ Tiling choose(int type, int64_t I, int64_t J, int64_t K, bool paired, bool may_s
     // latency of its loads), and how many of them a CU holds; measured over products of 59 x 64 x 300001 to
     // 8192 x 8192 x 8192.  Small tiles win wherever tiles are few or steps are: 512 x 1024 x 1024 takes 8 us in
     // tiles of 64 and 16 in tiles of 128; 8192 x 1024 x 4096 takes 71 in tiles of 128 and 94 in tiles of 64.
-    static const double full[kTileShapes] = {1.8, 0.55, 0.19, 0.62, 0.62};
-    static const double least[kTileShapes] = {1.9, 0.85, 0.50, 0.85, 0.85};
-    static const int held[kTileShapes] = {1, 2, 5, 2, 2};
+    static const double full[kTileShapes] = {1.8, 0.53, 0.19, 0.58, 0.58, 0.27};
+    static const double least[kTileShapes] = {1.9, 0.80, 0.50, 0.80, 0.80, 0.32};
+    static const int held[kTileShapes] = {1, 2, 5, 2, 2, 3};
     Tiling best{kTile64, 1, (int32_t)kt};
     double best_t = 1e300;
     for (int s = type == GS_TYPE_E4M3 ? kTile128 : kTile256; s < kTileShapes; s++) {
         const TileDims d = kTileDims[s];
         const int64_t tiles = div_up(I, d.bi) * div_up(cols, d.bj);
         // a tile's own start and end: its first loads and its epilogue, whose bytes grow with its area
-        const double ends = 1.5 + d.bi * d.bj / 8192.0;
+        const double ends = 1.0 + d.bi * d.bj / 6000.0;
         for (int64_t splits = 1; splits <= (may_split ? 2048 : 1); splits *= 2) {
             if (splits > 1 && (kt / splits < 4 || splits * I * J > (int64_t(1) << 26))) break;
             const int64_t per = div_up(kt, splits), each = div_up(tiles * splits, 256);
