@@ -1,0 +1,125 @@
+"""A neural decoder of Gaussian parameters: every Gaussian has a feature row, and a small network of
+gated residual blocks turns it into what the projection reads.
+
+    s_0 = features;  per block: y = norm(s), h = gated(y), s' = s + h W_down^T;
+    parameters [11 + 3 (d+1)^2][n] = base + (norm(s) W_head^T + b_head)^T
+
+The parameters' rows are those of gs_gaussians, one below the other (3 centre, 3 log-scale, 4 rotation, 1
+opacity logit, then the SH rows), so that the renderer reads the decoder's output and the decoder reads the
+gradients of gs_project_bwd in place.  Every step runs in the HIP library (gs_rmsnorm, gs_gated,
+gs_linear and their backward calls, gs_adam_step); torch owns memory and casts the float32 master weights
+to the operands' type once a step.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import adam, gsmi, neural
+
+
+class GaussianDecoder:
+    def __init__(self, renderer, width: int = 64, hidden: int = 128, blocks: int = 1, dtype=torch.bfloat16,
+                 lr: float = 1e-3, feature_lr: float = 1e-2, seed: int = 0):
+        r = self.renderer = renderer
+        n, dev = r.n, r.device
+        if n < 1:
+            raise ValueError("a decoder needs at least one Gaussian")
+        self.n, self.width, self.hidden, self.dtype = n, width, hidden, dtype
+        self.channels = 11 + r.sh.shape[0]
+        self.base = torch.cat([t.reshape(-1, n) for t in (r.means, r.log_scales, r.quats, r.logits, r.sh)]).contiguous()
+        self.params = self.base.clone()
+        self.dparams = torch.zeros_like(self.base)
+        g = torch.Generator(device=dev)
+        g.manual_seed(seed)
+        normal = lambda *s, std: torch.randn(*s, generator=g, device=dev) * std  # noqa: E731
+        # float32 masters; the head starts at zero, so that training starts from the base parameters
+        self.features = normal(n, width, std=1.0)
+        self.masters = []
+        for _ in range(blocks):
+            self.masters += [torch.ones(width, device=dev), normal(2 * hidden, width, std=1 / math.sqrt(width)),
+                             torch.zeros(2 * hidden, device=dev), normal(width, hidden, std=1 / math.sqrt(hidden))]
+        self.masters += [torch.ones(width, device=dev), torch.zeros(self.channels, width, device=dev),
+                         torch.zeros(self.channels, device=dev)]
+        self.blocks = [(neural.RmsNorm(n, width, dtype, device=dev),
+                        neural.GatedUnit(n, width, hidden, dtype, grad_dtype=torch.float32, backward=True, device=dev),
+                        neural.Linear(n, hidden, width, dtype, grad_dtype=torch.float32, backward=True, device=dev))
+                       for _ in range(blocks)]
+        self.norm = neural.RmsNorm(n, width, dtype, device=dev)
+        self.head = neural.Linear(n, width, self.channels, dtype, y_dtype=torch.float32, channel_major=True,
+                                  grad_dtype=torch.float32, backward=True, device=dev)
+        self.operands = [t.to(dtype) if t.dim() == 2 else t for t in self.masters]
+        self.features16 = torch.empty(n, width, dtype=dtype, device=dev)
+        # gradients in float32, in buffers that the optimizer keeps
+        self.grads = [torch.zeros_like(t) for t in self.masters]
+        self.dfeatures = torch.zeros_like(self.features)
+        state = lambda p, d, rate: adam.AdamState(p.numel(), [(p, d, 1, rate)], eps=1e-8)  # noqa: E731
+        self.states = [state(p, d, lr) for p, d in zip(self.masters, self.grads)] + [state(self.features, self.dfeatures, feature_lr)]
+        self._bind()
+
+    def _bind(self):
+        """The renderer reads its parameters from, and writes their gradients to, the decoder's rows."""
+        r, p, d = self.renderer, self.params, self.dparams
+        r.means, r.log_scales, r.quats, r.logits, r.sh = p[0:3], p[3:6], p[6:10], p[10], p[11:]
+        r.g = gsmi.gs_gaussians(self.n, r.means.data_ptr(), r.log_scales.data_ptr(), r.quats.data_ptr(), r.logits.data_ptr(),
+                                r.sh.data_ptr())
+        flat = d.view(-1)
+        n = self.n
+        r.d_means3, r.d_log_scales3, r.d_quats3 = flat[:3 * n], flat[3 * n:6 * n], flat[6 * n:10 * n]
+        r.d_logits3, r.d_sh3 = flat[10 * n:11 * n], flat[11 * n:]
+        r.g3 = gsmi.gs_grads3d(r.d_means3.data_ptr(), r.d_log_scales3.data_ptr(), r.d_quats3.data_ptr(), r.d_logits3.data_ptr(),
+                               r.d_sh3.data_ptr())
+
+    def forward(self):
+        """Decodes all Gaussians into self.params."""
+        for master, operand in zip(self.masters, self.operands):
+            if operand is not master:
+                operand.copy_(master)
+        self.features16.copy_(self.features)
+        self.kept = []
+        stream, branch = self.features16, None
+        for (norm, gated, down), k in zip(self.blocks, range(0, len(self.masters), 4)):
+            w_norm, w_in, b_in, w_down = self.operands[k:k + 4]
+            stream, y = norm.forward(stream, w_norm) if branch is None else norm.forward(branch, w_norm, stream)
+            h = gated.forward(y, w_in, b_in)
+            branch = down.forward(h, w_down)
+            self.kept.append((stream, y, h))
+        w_norm, w_head, b_head = self.operands[-3:]
+        stream, y = self.norm.forward(stream, w_norm) if branch is None else self.norm.forward(branch, w_norm, stream)
+        self.kept.append((stream, y, None))
+        self.head.forward(y, w_head, b_head, residual=self.base, out=self.params)
+        return self.params
+
+    def backward(self):
+        """Gradients of features and weights from self.dparams (gs_project_bwd's rows)."""
+        w_norm, w_head, b_head = self.operands[-3:]
+        stream, y, _ = self.kept[-1]
+        dy, dw, db = self.head.backward(y, w_head, self.dparams, b_head)
+        self.grads[-2].copy_(dw)
+        self.grads[-1].copy_(db)
+        ds, dw = self.norm.backward(stream, w_norm, dy)
+        self.grads[-3].copy_(dw)
+        for (norm, gated, down), k, (stream, y, h) in reversed(list(zip(self.blocks, range(0, len(self.masters), 4), self.kept))):
+            w_norm, w_in, b_in, w_down = self.operands[k:k + 4]
+            dh, dw, _ = down.backward(h, w_down, ds)
+            self.grads[k + 3].copy_(dw)
+            dy, dw, db = gated.backward(y, w_in, dh, b_in)
+            self.grads[k + 1].copy_(dw)
+            self.grads[k + 2].copy_(db)
+            ds, dw = norm.backward(stream, w_norm, dy, ds)
+            self.grads[k].copy_(dw)
+        self.dfeatures.copy_(ds)
+
+    def step(self):
+        """One training iteration: decode, render all views with their loss gradient, and take an Adam step."""
+        r = self.renderer
+        self.forward()
+        r.project()
+        r.bin()
+        r.fused(image=False, loss_sum=True)
+        r.project_backward()
+        self.backward()
+        for s in self.states:
+            s.step()
+        return r.loss_sum
