@@ -728,7 +728,7 @@ hipError_t launch_type(TileShape shape, Layout la, Layout lb, EpiKind kind, cons
 }
 
 // ---------------------------------------------------------------------------------------------------
-// Products of at most 64 rows: the bytes of b are the cost.  A workgroup takes 16 rows of b (16 gates and
+// Products of at most 32 rows: the bytes of b are the cost.  A workgroup takes 16 rows of b (16 gates and
 // their ups) and its waves take turns along k; both operands go from memory straight to the registers of
 // the matrix instruction, and the waves' sums meet in LDS.
 // ---------------------------------------------------------------------------------------------------
@@ -753,7 +753,7 @@ constexpr int kFewWaves = 8;
 
 template <class T, int FI, int EPI>
 __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(GemmArgs g) {
-    constexpr int NB = EPI == kEpiGated ? 2 : 1;
+    constexpr int NB = EPI == kEpiGated || EPI == kEpiDGated ? 2 : 1;
     constexpr int BK = 4 * T::chunk;  // k per step of a wave: one chunk per lane
     __shared__ f32x4 part[kFewWaves][FI * NB][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -802,11 +802,55 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(GemmArgs g) {
         for (int w = 0; w < kFewWaves; w++) v[b] += part[w][wave * NB + b][lane];
     }
     const int32_t i = wave * 16 + (lane & 15), j = j0 + (lane >> 4) * 4;
-    if (i >= g.I || j >= g.J) return;
-    if (EPI == kEpiGated)
-        epi_gated(g.e, v[0], v[NB - 1], i, j, g.J);
-    else
-        epi_linear(g.e, v[0], i, j, g.J);
+    if (EPI == kEpiLinear || EPI == kEpiGated) {
+        if (i >= g.I || j >= g.J) return;
+        if (EPI == kEpiGated)
+            epi_gated(g.e, v[0], v[NB - 1], i, j, g.J);
+        else
+            epi_linear(g.e, v[0], i, j, g.J);
+        return;
+    }
+    // the backward's projection: dz of four columns, and their sums over this wave's 16 rows
+    const Epi& e = g.e;
+    const bool in = i < g.I && j < g.J;
+    f32x4 s0 = {0.0f, 0.0f, 0.0f, 0.0f}, s1 = s0;
+    if (in) {
+        const f32x4 z = epi_pre(e, v[0], i, j, g.J, 0), d = epi_load(e.dy, e.dy_type, e.d_si, e.d_sj, i, j, g.J);
+        const f32x4 u = NB == 2 ? epi_pre(e, v[NB - 1], i, j, g.J, g.J) : z;
+        for (int k = 0; k < 4; k++) {
+            float a, da;
+            act_both(z[k], e.act, a, da);
+            const bool col = j + k < g.J;
+            s0[k] = col ? (NB == 2 ? d[k] * u[k] * da : d[k] * da) : 0.0f;
+            s1[k] = NB == 2 && col ? d[k] * a : 0.0f;
+        }
+        Epi f = e;
+        if (NB == 2) f.y_pad = 0;
+        epi_store(f, i, j, g.J, s0);
+        if (NB == 2) {  // the ups' columns, and after the last of them the padding of the row
+            const int64_t at = (int64_t)i * e.y_si + g.J;
+            for (int k = 0; k < 4; k++)
+                if (j + k < g.J) store_elem(e.y, e.y_type, at + j + k, s1[k]);
+            if (j + 4 >= g.J)
+                for (int32_t c = g.J; c < e.y_pad - g.J; c++) store_elem(e.y, e.y_type, at + c, 0.0f);
+        } else if (j + 4 >= g.J) {
+            for (int32_t c = j + 4; c < e.y_pad; c++) store_elem(e.y, e.y_type, (int64_t)i * e.y_si + c, 0.0f);
+        }
+    }
+    if (!e.colsum) return;
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1)
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            s0[k] += __shfl_xor(s0[k], m);
+            if (NB == 2) s1[k] += __shfl_xor(s1[k], m);
+        }
+    if ((lane & 15) == 0)
+        for (int k = 0; k < 4; k++)
+            if (j + k < g.J) {
+                e.colsum[(int64_t)wave * NB * g.J + j + k] = s0[k];
+                if (NB == 2) e.colsum[(int64_t)wave * NB * g.J + g.J + j + k] = s1[k];
+            }
 }
 
 // At most four rows: the matrix unit would leave three quarters of its rows empty and give a workgroup 16 rows
@@ -931,13 +975,19 @@ hipError_t launch_few_type(EpiKind kind, const GemmArgs& g, hipStream_t s) {
         if (g.I <= kHandful && g.J <= 1024) return launch_handful<T, kHandful, kEpiLinear>(g, s);
         if (g.I <= 16) return launch_few_one<T, 1, kEpiLinear>(g, s);
         if (g.I <= 32) return launch_few_one<T, 2, kEpiLinear>(g, s);
-        if (g.I <= 64) return launch_few_one<T, 4, kEpiLinear>(g, s);
     } else if (kind == kEpiGated) {
         if (g.I == 1) return launch_handful<T, 1, kEpiGated>(g, s);
         if (g.I <= kHandful && g.J <= 512) return launch_handful<T, kHandful, kEpiGated>(g, s);
         if (g.I <= 16) return launch_few_one<T, 1, kEpiGated>(g, s);
         if (g.I <= 32) return launch_few_one<T, 2, kEpiGated>(g, s);
-        if (g.I <= 64) return launch_few_one<T, 4, kEpiGated>(g, s);
+    } else if constexpr (T::chunk == 8) {
+        if (kind == kEpiDz) {
+            if (g.I <= 16) return launch_few_one<T, 1, kEpiDz>(g, s);
+            if (g.I <= 32) return launch_few_one<T, 2, kEpiDz>(g, s);
+        } else {
+            if (g.I <= 16) return launch_few_one<T, 1, kEpiDGated>(g, s);
+            if (g.I <= 32) return launch_few_one<T, 2, kEpiDGated>(g, s);
+        }
     }
     return hipErrorInvalidValue;
 }

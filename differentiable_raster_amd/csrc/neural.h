@@ -56,7 +56,7 @@ hipError_t launch_gemm_e4m3(TileShape shape, Layout la, Layout lb, EpiKind kind,
 hipError_t launch_gemm_reduce(const GemmArgs& g, hipStream_t s);
 
 // Products with at most kFewRows rows of a: every row of b is read once, no tile of a.
-constexpr int kFewRows = 64;
+constexpr int kFewRows = 32;
 hipError_t launch_few_rows(int type, EpiKind kind, const GemmArgs& g, hipStream_t s);
 hipError_t launch_few_rows_bf16(EpiKind kind, const GemmArgs& g, hipStream_t s);
 hipError_t launch_few_rows_f16(EpiKind kind, const GemmArgs& g, hipStream_t s);

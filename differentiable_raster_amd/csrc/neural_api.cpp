@@ -132,7 +132,13 @@ gs_status check_desc(const gs_linear_desc* d, bool gated, bool backward, Dims* o
     return GS_OK;
 }
 
-bool use_few_rows(const Dims& o) { return o.m <= kFewRows; }
+// The kernel of few rows gives a workgroup 16 columns and all of k: where columns are few and k is long it leaves
+// most of the card idle, and the tiled product with its split wins (backward of 34 rows, 2301 -> 128: 29 us against
+// 34; but of 14 rows, 5616 -> 6112: 91 against 82).  The gated unit has no split.  From 33 rows on the tiled product
+// reads x less often (64 rows, 4096 -> 4096: 19 us against 23).  Up to four rows have a wave per column and no limit.
+bool use_few_rows(const Dims& o, int32_t out, bool gated) {
+    return o.m <= 4 || (o.m <= kFewRows && (gated || out >= 1024 || o.k <= 1024));
+}
 
 Tiling forward_tiling(const gs_linear_desc* d, const Dims& o, bool gated) {
     if (gated) return choose(d->type, o.m, d->out, o.k, true, false);
@@ -146,7 +152,7 @@ struct ForwardWs {
 ForwardWs carve_forward(void* ws, const gs_linear_desc* d, const Dims& o, bool gated, size_t* bytes) {
     Carver c{static_cast<char*>(ws)};
     ForwardWs f{nullptr, nullptr, nullptr};
-    if (o.m > 0 && !use_few_rows(o)) {
+    if (o.m > 0 && !use_few_rows(o, d->out, gated)) {
         const size_t kp = (size_t)div_up(o.k, o.chunk) * 16;
         if (o.pack_x) f.x = c.take((size_t)o.m * kp);
         if (o.pack_w) f.w = c.take((size_t)o.n * kp);
@@ -215,7 +221,7 @@ gs_status forward(const gs_linear_desc* d, bool gated, const void* x, const floa
     const EpiKind kind = gated ? kEpiGated : kEpiLinear;
     const bool cm = d->y_channel_major != 0;
 
-    if (use_few_rows(o)) {
+    if (use_few_rows(o, d->out, gated)) {
         g.a = x, g.lda = o.ld_x, g.b = weight, g.ldb = o.ld_w;
         g.I = d->rows, g.J = d->out;
         g.e.y_si = cm ? 1 : o.ld_y, g.e.y_sj = cm ? o.ld_y : 1;
@@ -247,6 +253,7 @@ gs_status forward(const gs_linear_desc* d, bool gated, const void* x, const floa
 struct BackwardPlan {
     bool need_dz;      // dz is no array that the caller has: an own one, [rows][np]
     bool need_z;       // dz needs the pre-activation
+    bool few;          // which comes from the kernel of few rows
     int64_t kp, np;    // padded widths of x / weight copies and of dz
     Tiling tz, tx, tw;
     int64_t strips;    // rows of the column sums' partials out of the z product or the copy of dy
@@ -276,7 +283,8 @@ BackwardPlan plan_backward(const gs_linear_desc* d, const Dims& o, bool gated, v
     p.tx = choose(d->type, o.m > 0 ? o.m : 1, o.k, o.n, false, true);
     p.tw = choose(d->type, o.n, o.k, o.m, false, true);
     const TileDims td = kTileDims[p.tz.shape];
-    p.strips = p.need_z ? div_up(o.m > 0 ? o.m : 1, td.bi) * td.wi : pack_row_blocks(o.m);
+    p.few = p.need_z && use_few_rows(o, d->out, gated);
+    p.strips = p.few ? div_up(o.m, 16) : p.need_z ? div_up(o.m > 0 ? o.m : 1, td.bi) * td.wi : pack_row_blocks(o.m);
     if (o.pack_x) p.x = c.take((size_t)o.m * p.kp * es);
     if (o.pack_w) p.w = c.take((size_t)o.n * p.kp * es);
     if (p.need_dz) p.dz = c.take((size_t)o.m * p.np * es);
@@ -328,27 +336,34 @@ gs_status backward(const gs_linear_desc* d, bool gated, const void* x, const voi
             e = launch_colsum(p.sums, GS_TYPE_F32, o.n, p.narrow.db_rows, (int32_t)o.n, static_cast<float*>(p.sums2), dbias, s);
         return launched(e, "backward of a narrow map");
     }
+    const void *xo = x, *wo = weight;    // what the tiled products read
+    const void *zx = nullptr, *zw = nullptr;  // what the projection reads: the kernel of few rows takes any strides
+    int64_t ld_zx = 0, ld_zw = 0;
     if (o.m > 0) {
-        e = copy_operands(d, o, x, weight, o.pack_x && (p.need_z || dweight) ? p.x : nullptr,
-                          o.pack_w && (p.need_z || dx) ? p.w : nullptr, p.kp, s);
+        const bool tiled_z = p.need_z && !p.few;
+        const Dims given = o;
+        e = copy_operands(d, o, xo, wo, o.pack_x && (tiled_z || dweight) ? p.x : nullptr,
+                          o.pack_w && (tiled_z || dx) ? p.w : nullptr, p.kp, s);
         if (e != hipSuccess) return launched(e, "operand copy");
+        if (p.few) zx = x, zw = weight, ld_zx = given.ld_x, ld_zw = given.ld_w;
     }
-    const void *xo = x, *wo = weight;
     const int64_t ldx = o.ld_x, ldw = o.ld_w;
+    if (!p.few) zx = xo, zw = wo, ld_zx = ldx, ld_zw = ldw;
     const int64_t d_si = cm ? 1 : o.ld_y, d_sj = cm ? o.ld_y : 1;
 
     // dz, and the column sums of its unrounded values
     if (o.m > 0 && p.need_z) {
         GemmArgs g;
         std::memset(&g, 0, sizeof(g));
-        g.a = xo, g.lda = ldx, g.b = wo, g.ldb = ldw;
+        g.a = zx, g.lda = ld_zx, g.b = zw, g.ldb = ld_zw;
         g.I = d->rows, g.J = d->out, g.K = o.k;
         g.e.y = p.dz, g.e.y_si = p.np, g.e.y_sj = 1, g.e.y_type = d->type, g.e.y_pad = (int32_t)p.np;
         g.e.bias = bias, g.e.act = d->act;
         g.e.dy = dy, g.e.dy_type = d->y_type, g.e.d_si = d_si, g.e.d_sj = d_sj;
         g.e.colsum = dbias ? static_cast<float*>(p.sums) : nullptr;
         set_tiling(g, p.tz, nullptr);
-        e = tiled(d->type, p.tz, kRowK, kRowK, gated ? kEpiDGated : kEpiDz, g, s);
+        const EpiKind kind = gated ? kEpiDGated : kEpiDz;
+        e = p.few ? launch_few_rows(d->type, kind, g, s) : tiled(d->type, p.tz, kRowK, kRowK, kind, g, s);
         if (e != hipSuccess) return launched(e, "projection of the backward");
     } else if (o.m > 0 && p.need_dz) {
         if (!cm && !dbias) {
