@@ -55,6 +55,28 @@ __device__ __forceinline__ float row_sum(float v, float* lds) {
     }
     return v;
 }
+// Two sums at once: one exchange through LDS.
+template <int NT>
+__device__ __forceinline__ void row_sums(float& a, float& b, float* lds) {
+#pragma unroll
+    for (int m = 1; m < (NT < 64 ? NT : 64); m <<= 1) {
+        a += __shfl_xor(a, m);
+        b += __shfl_xor(b, m);
+    }
+    if (NT > 64) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) {
+            lds[threadIdx.x >> 6] = a;
+            lds[16 + (threadIdx.x >> 6)] = b;
+        }
+        __syncthreads();
+        a = b = 0.0f;
+        for (int w = 0; w < NT / 64; w++) {
+            a += lds[w];
+            b += lds[16 + w];
+        }
+    }
+}
 template <int NT>
 __device__ __forceinline__ uint32_t row_umax(uint32_t v, float* lds) {
 #pragma unroll
@@ -79,8 +101,8 @@ __device__ __forceinline__ float to_range(float v) {  // NaN stays NaN
     return v > kE4m3Max ? kE4m3Max : (v < -kE4m3Max ? -kE4m3Max : v);
 }
 
-constexpr int rows_per_block(int nt) { return nt < 256 ? 256 / nt : 1; }
-constexpr int block_of(int nt) { return nt < 256 ? 256 : nt; }
+constexpr int rows_per_block(int nt) { return nt <= 64 ? 256 / nt : 1; }
+constexpr int block_of(int nt) { return nt <= 64 ? 256 : nt; }
 
 // NT threads per row, NC chunks of 8 values per thread.
 template <class T, int NT, int NC>
@@ -163,7 +185,7 @@ __global__ __launch_bounds__(block_of(NT)) void norm_fwd_kernel(NormArgs a) {
 template <class T, int NT, int NC>
 __global__ __launch_bounds__(block_of(NT)) void norm_bwd_kernel(NormArgs a) {
     constexpr int RPB = rows_per_block(NT), WIDTH = NT * NC * 8;
-    __shared__ float lds[16];
+    __shared__ float lds[32];
     __shared__ float shares[RPB > 1 ? RPB * WIDTH : 1];
     const int64_t group = (int64_t)blockIdx.x * RPB + threadIdx.x / NT, groups = (int64_t)gridDim.x * RPB;
     const int t = threadIdx.x % NT;
@@ -191,8 +213,9 @@ __global__ __launch_bounds__(block_of(NT)) void norm_bwd_kernel(NormArgs a) {
                 sq = fmaf(s[c][k], s[c][k], sq);
                 dot = fmaf(g[c][k] * w[c][k], s[c][k], dot);
             }
-        const float rstd = 1.0f / sqrtf(row_sum<NT>(sq, lds) / (float)a.width + a.eps);
-        const float mean = row_sum<NT>(dot, lds) * rstd / (float)a.width;  // mean of dy weight n
+        row_sums<NT>(sq, dot, lds);
+        const float rstd = 1.0f / sqrtf(sq / (float)a.width + a.eps);
+        const float mean = dot * rstd / (float)a.width;  // mean of dy weight n
 #pragma unroll
         for (int c = 0; c < NC; c++) {
             for (int k = 0; k < 8; k++) {
@@ -223,16 +246,33 @@ __global__ __launch_bounds__(block_of(NT)) void norm_bwd_kernel(NormArgs a) {
     }
 }
 
-// Threads per row and chunks per thread by the row's width.
+// Threads per row and chunks per thread by the row's width.  The backward holds five rows of a chunk where the
+// forward holds two, so it takes one chunk per thread for longer (16384 x 2048: 83 us with four chunks of 64
+// threads, against 57 with one chunk of 256).
 struct RowShape {
     int nt, nc;
 };
-RowShape row_shape(int32_t width) {
+RowShape backward_shape(int32_t width) {
+    if (width <= 32) return {4, 1};
     if (width <= 64) return {8, 1};
     if (width <= 128) return {16, 1};
     if (width <= 256) return {32, 1};
     if (width <= 512) return {64, 1};
+    if (width <= 1024) return {128, 1};
+    if (width <= 2048) return {256, 1};
+    if (width <= 4096) return {512, 1};
+    if (width <= 8192) return {1024, 1};
+    return {1024, 4};
+}
+RowShape row_shape(int32_t width) {
+    if (width <= 32) return {4, 1};
+    if (width <= 64) return {8, 1};
+    if (width <= 128) return {16, 1};
+    if (width <= 256) return {32, 1};
+    if (width <= 512) return {64, 1};
+    if (width <= 1024) return {64, 2};
     if (width <= 2048) return {64, 4};
+    if (width <= 4096) return {256, 2};
     if (width <= 8192) return {256, 4};
     return {1024, 4};
 }
@@ -252,20 +292,28 @@ hipError_t bwd_one(const NormArgs& a, int32_t blocks, hipStream_t s) {
 template <class T>
 hipError_t fwd_type(const NormArgs& a, hipStream_t s) {
     const RowShape r = row_shape(a.width);
+    if (r.nt == 4) return fwd_one<T, 4, 1>(a, s);
     if (r.nt == 8) return fwd_one<T, 8, 1>(a, s);
     if (r.nt == 16) return fwd_one<T, 16, 1>(a, s);
     if (r.nt == 32) return fwd_one<T, 32, 1>(a, s);
-    if (r.nt == 64) return r.nc == 1 ? fwd_one<T, 64, 1>(a, s) : fwd_one<T, 64, 4>(a, s);
-    return r.nt == 256 ? fwd_one<T, 256, 4>(a, s) : fwd_one<T, 1024, 4>(a, s);
+    if (r.nt == 64) return r.nc == 1 ? fwd_one<T, 64, 1>(a, s) : r.nc == 2 ? fwd_one<T, 64, 2>(a, s) : fwd_one<T, 64, 4>(a, s);
+    if (r.nt == 256) return r.nc == 2 ? fwd_one<T, 256, 2>(a, s) : fwd_one<T, 256, 4>(a, s);
+    return fwd_one<T, 1024, 4>(a, s);
 }
 template <class T>
 hipError_t bwd_type(const NormArgs& a, int32_t blocks, hipStream_t s) {
-    const RowShape r = row_shape(a.width);
-    if (r.nt == 8) return bwd_one<T, 8, 1>(a, blocks, s);
-    if (r.nt == 16) return bwd_one<T, 16, 1>(a, blocks, s);
-    if (r.nt == 32) return bwd_one<T, 32, 1>(a, blocks, s);
-    if (r.nt == 64) return r.nc == 1 ? bwd_one<T, 64, 1>(a, blocks, s) : bwd_one<T, 64, 4>(a, blocks, s);
-    return r.nt == 256 ? bwd_one<T, 256, 4>(a, blocks, s) : bwd_one<T, 1024, 4>(a, blocks, s);
+    const RowShape r = backward_shape(a.width);
+    switch (r.nt) {
+        case 4: return bwd_one<T, 4, 1>(a, blocks, s);
+        case 8: return bwd_one<T, 8, 1>(a, blocks, s);
+        case 16: return bwd_one<T, 16, 1>(a, blocks, s);
+        case 32: return bwd_one<T, 32, 1>(a, blocks, s);
+        case 64: return bwd_one<T, 64, 1>(a, blocks, s);
+        case 128: return bwd_one<T, 128, 1>(a, blocks, s);
+        case 256: return bwd_one<T, 256, 1>(a, blocks, s);
+        case 512: return bwd_one<T, 512, 1>(a, blocks, s);
+        default: return r.nc == 1 ? bwd_one<T, 1024, 1>(a, blocks, s) : bwd_one<T, 1024, 4>(a, blocks, s);
+    }
 }
 
 // ---- operand copies -------------------------------------------------------------------------------
@@ -455,8 +503,8 @@ hipError_t launch_norm_fwd(int type, const NormArgs& a, hipStream_t s) {
 
 // Workgroups of the backward: enough to fill the card, few enough that their partial sums cost little.
 int32_t norm_blocks(int64_t rows, int32_t width) {
-    const RowShape s = row_shape(width);
-    const int64_t blocks = (rows + rows_per_block(s.nt) - 1) / rows_per_block(s.nt), most = s.nt >= 256 ? 1024 : 2048;
+    const RowShape s = backward_shape(width);
+    const int64_t blocks = (rows + rows_per_block(s.nt) - 1) / rows_per_block(s.nt), most = (int64_t)256 * 2048 / block_of(s.nt);
     return (int32_t)(blocks < most ? blocks : most);
 }
 
