@@ -84,6 +84,21 @@ struct NarrowShape {
 NarrowShape narrow_shape(int64_t rows, int64_t k, int64_t n, bool gated, bool activated);
 hipError_t launch_narrow(int type, const NarrowArgs& a, bool gated, const NarrowShape& p, hipStream_t s);
 
+// The forward of a narrow map over many rows, operands of any stride and width, 16-bit types.
+struct NarrowFwdArgs {
+    const void *x, *w;
+    int64_t ldx, ldw;
+    int32_t rows, k, n;     // n: result columns (gated: half of the weight rows)
+    const float* bias;
+    int32_t act;
+    const void* res;        // optional
+    void* y;
+    int64_t ld_r, ld_y;
+    int32_t y_type;
+};
+bool narrow_fwd_serves(int64_t rows, int64_t k, int64_t out, bool gated, bool copies);
+hipError_t launch_narrow_fwd(int type, const NarrowFwdArgs& a, bool gated, hipStream_t s);
+
 // Copies of operands into the layout that the tiled product reads: dst[r][c] = src[r * s_row + c] for c < cols
 // and 0 for c in [cols, ld); ld a multiple of 16 bytes.  One or two operands in one launch.
 struct PackJob {

@@ -140,6 +140,10 @@ bool use_few_rows(const Dims& o, int32_t out, bool gated) {
     return o.m <= 4 || (o.m <= kFewRows && (gated || out >= 1024 || o.k <= 1024));
 }
 
+bool use_narrow(const gs_linear_desc* d, const Dims& o, bool gated) {
+    return d->type != GS_TYPE_E4M3 && !d->y_channel_major && narrow_fwd_serves(o.m, o.k, d->out, gated, o.pack_x || o.pack_w);
+}
+
 Tiling forward_tiling(const gs_linear_desc* d, const Dims& o, bool gated) {
     if (gated) return choose(d->type, o.m, d->out, o.k, true, false);
     if (d->y_channel_major) return choose(d->type, o.n, o.m, o.k, false, true);
@@ -152,7 +156,7 @@ struct ForwardWs {
 ForwardWs carve_forward(void* ws, const gs_linear_desc* d, const Dims& o, bool gated, size_t* bytes) {
     Carver c{static_cast<char*>(ws)};
     ForwardWs f{nullptr, nullptr, nullptr};
-    if (o.m > 0 && !use_few_rows(o, d->out, gated)) {
+    if (o.m > 0 && !use_few_rows(o, d->out, gated) && !use_narrow(d, o, gated)) {
         const size_t kp = (size_t)div_up(o.k, o.chunk) * 16;
         if (o.pack_x) f.x = c.take((size_t)o.m * kp);
         if (o.pack_w) f.w = c.take((size_t)o.n * kp);
@@ -228,6 +232,15 @@ gs_status forward(const gs_linear_desc* d, bool gated, const void* x, const floa
         g.e.r_si = cm ? 1 : o.ld_r, g.e.r_sj = cm ? o.ld_r : 1;
         g.e.scale_i = x_scale, g.e.scale_j = w_scale;
         return launched(launch_few_rows(d->type, kind, g, s), "product of few rows");
+    }
+    if (use_narrow(d, o, gated)) {
+        NarrowFwdArgs a;
+        std::memset(&a, 0, sizeof(a));
+        a.x = x, a.w = weight, a.ldx = o.ld_x, a.ldw = o.ld_w;
+        a.rows = d->rows, a.k = d->in, a.n = d->out;
+        a.bias = bias, a.act = d->act, a.res = residual;
+        a.y = y, a.ld_r = o.ld_r, a.ld_y = o.ld_y, a.y_type = d->y_type;
+        return launched(launch_narrow_fwd(d->type, a, gated, s), "product of a narrow map");
     }
     const int64_t kp = div_up(o.k, o.chunk) * o.chunk;
     hipError_t e = copy_operands(d, o, x, weight, f.x, f.w, kp, s);

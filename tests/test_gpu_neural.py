@@ -527,3 +527,57 @@ def test_narrow_backward(env, rows, k, n, gated, act, ytype, bias, cm):
     # views with rows further apart, NaN between them
     xs, ws, dys = strided(torch, x, 8), strided(torch, w, 16), strided(torch, dy, 4)
     assert all(torch.equal(p, q) for p, q in zip(first, plan.backward(xs, ws, dys, b)))
+
+
+NARROW_FWD = [  # rows, in, out (hidden), gated, act, y, bias, residual, channel_major
+    (16384, 64, 59, False, "none", "f32", True, True, True),
+    (16389, 63, 59, False, "none", "f32", False, False, True),
+    (16385, 53, 48, False, "gelu", "bf16", True, True, False),
+    (16411, 8, 3, False, "relu", "f32", True, False, False),
+    (20001, 30, 64, False, "silu", "bf16", False, True, False),
+    (16390, 64, 17, False, "none", "f16", True, True, False),
+    (16391, 127, 64, False, "silu", "f16", True, False, False),
+    (16400, 97, 33, False, "none", "f32", True, True, False),
+    (70001, 36, 16, True, "gelu", "bf16", True, False, False),
+    (16399, 64, 32, True, "silu", "bf16", True, False, False),
+    (16399, 115, 27, True, "relu", "f16", False, False, False),
+    (16384, 53, 31, True, "none", "f32", True, False, False),
+]
+
+
+@pytest.mark.parametrize("rows,k,n,gated,act,ytype,bias,residual,cm", NARROW_FWD)
+def test_narrow_forward(env, rows, k, n, gated, act, ytype, bias, residual, cm):
+    """Many rows of a narrow map: the forward straight from memory to fragments."""
+    torch, gsmi, neural = env
+    dtype = "f16" if ytype == "f16" else "bf16"
+    yt = dt(torch, ytype)
+    normal, x, w, b, _, _, x64, w64, z, e_z = make_product(torch, rows, k, 2 * n if gated else n, dtype, 23 * rows + k, bias)
+    if gated:
+        g, u, v, _, _, e_u, e_a = gated_parts(torch, z, e_z, n, act)
+        want = v * u
+        e = e_a * (u.abs() + e_u) + v.abs() * e_u + 2.0 ** -23 * want.abs()
+        bound = e + U[ytype] * (want.abs() + e) + TINY[ytype]
+        plan = neural.GatedUnit(rows, k, n, dt(torch, dtype), act=act, y_dtype=yt)
+        run = lambda x, w, out=None: plan.forward(x, w, b, out=out)  # noqa: E731
+        r = None
+    else:
+        v, _ = act64(torch, z, act)
+        e = e_z if act == "none" else 1.13 * e_z + 4e-6 * (1 + z.abs())
+        if cm:
+            v, e = v.t(), e.t()
+        r = normal(*((n, rows) if cm else (rows, n))).to(yt) if residual else None
+        want = v + (r.double() if residual else 0)
+        bound = e + 2.0 ** -23 * (v.abs() + want.abs()) + U[ytype] * (want.abs() + e) + TINY[ytype]
+        plan = neural.Linear(rows, k, n, dt(torch, dtype), act=act, y_dtype=yt, channel_major=cm)
+        run = lambda x, w, out=None: plan.forward(x, w, b, r, out=out)  # noqa: E731
+    y = run(x, w).clone()
+    within(torch, y, want, bound, "y")
+    # views with rows further apart (NaN between them), and a result inside a wider array
+    xs, ws = strided(torch, x, 3), strided(torch, w, 5)
+    wide = torch.full((y.shape[0], y.shape[1] + 3), 7.0, device="cuda").to(yt)
+    run(xs, ws, wide[:, :y.shape[1]])
+    assert torch.equal(wide[:, :y.shape[1]], y) and bool((wide[:, y.shape[1]:] == 7).all())
+    if residual:
+        out = r.clone()
+        plan.forward(x, w, b, out, out=out)
+        assert torch.equal(out, y)
