@@ -143,6 +143,19 @@ def test_norm_backward(env, rows, width, dtype, pad, through):
     assert abs(float((dx.double() * v).sum()) - diff) <= bound
 
 
+def test_norm_rows_past_one_axis(env):
+    """More workgroups than one axis of a launch takes: short rows, 64 to a workgroup."""
+    torch, gsmi, neural = env
+    rows = (1 << 27) + 64 * 5 + 3
+    x = torch.empty(rows, 2, dtype=torch.bfloat16, device="cuda")
+    x.normal_()
+    w = torch.tensor([0.5, 2.0], device="cuda")
+    _, y = neural.RmsNorm(rows, 2, torch.bfloat16, eps=1e-5).forward(x, w)
+    at = torch.cat([torch.arange(0, 100), torch.arange((1 << 27) - 100, rows)]).cuda()
+    y64, _ = norm_reference(torch, x[at].double(), w.double(), 1e-5)
+    within(torch, y[at], y64, (2.0 ** -8 + 41 * 2.0 ** -24) * y64.abs() + 1e-38, "y")
+
+
 def test_norm_special_rows(env):
     """Rows of zeros, a row with a NaN, one with an infinity: only those rows are touched."""
     torch, gsmi, neural = env
