@@ -366,6 +366,18 @@ __device__ __forceinline__ void tile_of(int32_t id, int32_t ni, int32_t nj, int3
     tj = in / h;
 }
 
+// One tile of the result per workgroup, 128 bytes of k per step, one tile in LDS while the other is filled; three
+// forms of the loop, by how many products a step has to hide its loads and its LDS reads behind.
+//   Tiles of 256 (512 threads, one workgroup per CU): bound by the matrix unit and, between tiles, by the epilogue,
+// which nothing overlaps.  8192^3 in bf16: 960 us = 1145 TF (a library product of it: 1365).  8192 x 2048 x 16384
+// with the gated derivative's epilogue, which reads 134 MB and writes 268 MB: 690 us, of which the matrix unit is
+// busy for 40 %; the two gradient products of that size 478 and 545 us = 1150 and 1008 TF.
+//   Tiles of 128 (two or three per CU): the LDS reads of a step, 64 KB per 128 x 128 x 64, take as long as its
+// products.  8192 x 4096 x 1024: 75 us = 920 TF.  In 8 bits the same bytes hold twice the products at twice the rate:
+// 8192 x 1024 x 8192 gated 103 us = 1336 TF, bound by LDS and the tile's ends (8 steps a tile); a tile of 256 of that
+// type spills.
+//   Tiles of 64: many tiles of one or two steps, bound by memory.  59 x 64 x 1000000 onto a residual: 132 us for
+// 600 MB = 4.5 TB/s, against 5.1 of a copy.
 template <class T, int SHAPE, int LA, int LB, int EPI>
 __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256, 2) void gemm_kernel(GemmArgs g) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host needs the kernel's name alone
@@ -730,7 +742,8 @@ hipError_t launch_type(TileShape shape, Layout la, Layout lb, EpiKind kind, cons
 // ---------------------------------------------------------------------------------------------------
 // Products of at most 32 rows: the bytes of b are the cost.  A workgroup takes 16 rows of b (16 gates and
 // their ups) and its waves take turns along k; both operands go from memory straight to the registers of
-// the matrix instruction, and the waves' sums meet in LDS.
+// the matrix instruction, and the waves' sums meet in LDS.  4 rows, 1024 -> 2 x 4096 gated: 6.0 us for 17 MB; two
+// thirds of that is the launch and the latency of the first loads.
 // ---------------------------------------------------------------------------------------------------
 template <class T>
 __device__ __forceinline__ u32x4 row_chunk(const char* row, bool in, int64_t k, int64_t K) {
@@ -855,7 +868,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(GemmArgs g) {
 
 // At most four rows: the matrix unit would leave three quarters of its rows empty and give a workgroup 16 rows
 // of b, which keeps most CUs idle where b has 1024 rows.  Here 64 lanes share one row of b (one gate and its up)
-// and `split` waves its summed axis, the sums are float32 multiply-adds.
+// and `split` waves its summed axis, the sums are float32 multiply-adds.  1 row, 4096 -> 1024: 5.4 us for 8.4 MB, the
+// latency of a launch, one load and six exchanges between lanes; the bytes alone would be 1.7.
 template <class T>
 __device__ __forceinline__ void chunk_values(u32x4 c, float (&v)[T::chunk]) {
     if constexpr (T::chunk == 8) {

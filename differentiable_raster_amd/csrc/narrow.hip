@@ -1,6 +1,6 @@
 // Narrow linear maps and gated units over many rows: the backward (x of at most 64 or 128 columns, at most 256
-// weight rows) in one pass, and the forward below.  Backward: per block of 64 rows the pre-activation is computed again, dz takes its place in
-// LDS, and dx and the block's share of dweight come from there.
+// weight rows) in one pass, and the forward below.  Backward: per block of 64 rows the pre-activation is computed
+// again, dz takes its place in LDS, and dx and the block's share of dweight come from there.
 //
 //   z = x W^T + b,  dz = dy act'(z)  (gated: dgate = dh u act'(g), dup = dh act(g)),
 //   dx = dz W,  dW = sum over rows of dz^T x,  db = sum over rows of dz.
@@ -9,6 +9,10 @@
 // and 256 weight rows) and read it and x twice more.  Here x and dy are read once, dx is written once, the
 // weights stay in registers as fragments of both products, and dW stays in the accumulators of a persistent
 // workgroup, whose share is added up afterwards in a fixed order.
+// 300001 x 64 -> 59 without an activation, float32 channel-major dy: 36 us for 148 MB = 4.1 TB/s.  262144 x 64 -> 2 x 128
+// gated: 91 us for 134 MB; there the activations (38 us of vector instructions), the LDS reads (28 us) and the matrix
+// instructions (11 us) are in phases between barriers.  The two waves of a SIMD take two of the phases in opposite
+// order, so that one's matrix instructions meet the other's vector instructions.
 #include <type_traits>
 
 #include "elem.h"
