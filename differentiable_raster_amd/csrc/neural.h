@@ -53,7 +53,15 @@ hipError_t launch_gemm(int type, TileShape shape, Layout la, Layout lb, EpiKind 
 hipError_t launch_gemm_bf16(TileShape shape, Layout la, Layout lb, EpiKind kind, const GemmArgs& g, hipStream_t s);
 hipError_t launch_gemm_f16(TileShape shape, Layout la, Layout lb, EpiKind kind, const GemmArgs& g, hipStream_t s);
 hipError_t launch_gemm_e4m3(TileShape shape, Layout la, Layout lb, EpiKind kind, const GemmArgs& g, hipStream_t s);
-hipError_t launch_gemm_reduce(const GemmArgs& g, hipStream_t s);
+// The join of a split product; in the same launch, if rows of shares go with it, their sums.
+struct ShareSum {  // out[c] = sum_r in[r * cols + c]; out null: none
+    const float* in;
+    int64_t rows;
+    int32_t cols;
+    float* out;
+};
+hipError_t launch_gemm_reduce(const GemmArgs& g, const ShareSum& c, hipStream_t s);
+hipError_t launch_share_sum(const ShareSum& c, hipStream_t s);
 
 // Products with at most kFewRows rows of a: every row of b is read once, no tile of a.
 constexpr int kFewRows = 32;
@@ -114,7 +122,8 @@ hipError_t launch_pack_rows(int from, int to, const PackJob* jobs, int count, hi
 int64_t pack_row_blocks(int64_t rows);
 hipError_t launch_pack(const void* src, int src_type, int64_t s_row, int64_t s_col, int64_t rows, int32_t cols,
                        void* dst, int dst_type, int64_t ld_dst, float* sums, hipStream_t s);
-// out[c] = sum_r in[r * s_row + c], in a fixed order.  partial: colsum_partial_floats(rows, cols) floats.
+// out[c] = sum_r in[r * s_row + c], in a fixed order.  partial: colsum_partial_floats(rows, cols) floats.  For rows of
+// shares, few or float32, launch_share_sum is the shorter way.
 size_t colsum_partial_floats(int64_t rows, int32_t cols);
 hipError_t launch_colsum(const void* in, int type, int64_t s_row, int64_t rows, int32_t cols, float* partial, float* out,
                          hipStream_t s);

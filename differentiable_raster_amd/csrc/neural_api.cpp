@@ -84,10 +84,14 @@ void set_tiling(GemmArgs& g, const Tiling& t, void* partial) {
     g.partial = t.splits > 1 ? static_cast<float*>(partial) : nullptr;
 }
 
-hipError_t tiled(int type, const Tiling& t, Layout la, Layout lb, EpiKind kind, const GemmArgs& g, hipStream_t s) {
+constexpr ShareSum kNoShares{nullptr, 0, 0, nullptr};
+
+// shares: of an earlier launch, to be added up beside the join
+hipError_t tiled(int type, const Tiling& t, Layout la, Layout lb, EpiKind kind, const GemmArgs& g, hipStream_t s,
+                 const ShareSum& shares = kNoShares) {
     hipError_t e = launch_gemm(type, t.shape, la, lb, kind, g, s);
-    if (e == hipSuccess && g.partial) e = launch_gemm_reduce(g, s);
-    return e;
+    if (e == hipSuccess && g.partial) return launch_gemm_reduce(g, shares, s);
+    return e == hipSuccess && shares.out ? launch_share_sum(shares, s) : e;
 }
 
 // ---------------------------------------------------------------------------------------------------
@@ -275,6 +279,11 @@ struct BackwardPlan {
     size_t bytes;
 };
 
+// Up to 4096 strips one launch of few columns per workgroup adds them up in less time than two of parts and their
+// sums (2048 x 256: 6 us against 9), and it can go with the join of dweight (backward of 300001 x 64 -> 59: 57 us with
+// two launches of its own for dbias, 50 without).
+bool sums_at_once(const BackwardPlan& p) { return p.need_dz && p.strips <= 4096; }
+
 BackwardPlan plan_backward(const gs_linear_desc* d, const Dims& o, bool gated, void* ws) {
     BackwardPlan p;
     std::memset(&p, 0, sizeof(p));
@@ -284,7 +293,6 @@ BackwardPlan plan_backward(const gs_linear_desc* d, const Dims& o, bool gated, v
     if (p.narrow.kp) {
         p.partial = c.take((size_t)p.narrow.groups * o.n * o.k * 4);
         p.sums = c.take((size_t)p.narrow.db_rows * o.n * 4);
-        p.sums2 = c.take(colsum_partial_floats(p.narrow.db_rows, (int32_t)o.n) * 4);
         p.bytes = c.used;
         return p;
     }
@@ -302,7 +310,7 @@ BackwardPlan plan_backward(const gs_linear_desc* d, const Dims& o, bool gated, v
     if (o.pack_w) p.w = c.take((size_t)o.n * p.kp * es);
     if (p.need_dz) p.dz = c.take((size_t)o.m * p.np * es);
     if (p.need_dz) p.sums = c.take((size_t)p.strips * o.n * 4);
-    p.sums2 = c.take(colsum_partial_floats(p.need_dz ? p.strips : o.m, (int32_t)o.n) * 4);
+    if (!sums_at_once(p)) p.sums2 = c.take(colsum_partial_floats(p.need_dz ? p.strips : o.m, (int32_t)o.n) * 4);
     const size_t px = p.tx.partial_bytes(o.m, o.k), pw = p.tw.partial_bytes(o.n, o.k);
     p.partial = c.take(px > pw ? px : pw);
     p.bytes = c.used;
@@ -338,15 +346,16 @@ gs_status backward(const gs_linear_desc* d, bool gated, const void* x, const voi
         a.dw_partial = dweight ? static_cast<float*>(p.partial) : nullptr;
         a.db_partial = dbias ? static_cast<float*>(p.sums) : nullptr;
         e = launch_narrow(d->type, a, gated, p.narrow, s);
+        const ShareSum shares{a.db_partial, p.narrow.db_rows, (int32_t)o.n, dbias};
         if (e == hipSuccess && dweight) {
             GemmArgs g;
             std::memset(&g, 0, sizeof(g));
             g.I = (int32_t)o.n, g.J = d->in, g.splits = p.narrow.groups, g.partial = a.dw_partial;
             g.e.y = dweight, g.e.y_si = o.k, g.e.y_sj = 1, g.e.y_type = d->grad_type;
-            e = launch_gemm_reduce(g, s);
+            e = launch_gemm_reduce(g, shares, s);
+        } else if (e == hipSuccess && dbias) {
+            e = launch_share_sum(shares, s);
         }
-        if (e == hipSuccess && dbias)
-            e = launch_colsum(p.sums, GS_TYPE_F32, o.n, p.narrow.db_rows, (int32_t)o.n, static_cast<float*>(p.sums2), dbias, s);
         return launched(e, "backward of a narrow map");
     }
     const void *xo = x, *wo = weight;    // what the tiled products read
@@ -388,8 +397,11 @@ gs_status backward(const gs_linear_desc* d, bool gated, const void* x, const voi
         }
         if (e != hipSuccess) return launched(e, "gradient copy");
     }
+    ShareSum shares = kNoShares;
     if (dbias) {
-        if (p.need_dz)
+        if (sums_at_once(p))
+            shares = ShareSum{static_cast<const float*>(p.sums), o.m > 0 ? p.strips : 0, (int32_t)o.n, dbias};
+        else if (p.need_dz)
             e = launch_colsum(p.sums, GS_TYPE_F32, o.n, o.m > 0 ? p.strips : 0, (int32_t)o.n, static_cast<float*>(p.sums2), dbias, s);
         else
             e = launch_colsum(dy, d->y_type, o.ld_y, o.m, (int32_t)o.n, static_cast<float*>(p.sums2), dbias, s);
@@ -414,8 +426,10 @@ gs_status backward(const gs_linear_desc* d, bool gated, const void* x, const voi
         g.I = (int32_t)o.n, g.J = d->in, g.K = o.m, g.a_cols = (int32_t)p.np, g.b_cols = (int32_t)p.kp;
         g.e.y = dweight, g.e.y_si = o.k, g.e.y_sj = 1, g.e.y_type = d->grad_type;
         set_tiling(g, p.tw, p.partial);
-        e = tiled(d->type, p.tw, kRowFree, kRowFree, kEpiLinear, g, s);
+        e = tiled(d->type, p.tw, kRowFree, kRowFree, kEpiLinear, g, s, shares);
         if (e != hipSuccess) return launched(e, "weight gradient");
+    } else if (shares.out) {
+        return launched(launch_share_sum(shares, s), "bias gradient");
     }
     return GS_OK;
 }
@@ -494,7 +508,7 @@ size_t gs_rmsnorm_bwd_workspace_size(const gs_norm_desc* d) {
     NormArgs a;
     if (check_norm(d, &a) != GS_OK) return 0;
     const int32_t blocks = norm_blocks(d->rows, d->width);
-    return align256((size_t)blocks * d->width * 4) + align256(colsum_partial_floats(blocks, d->width) * 4);
+    return align256((size_t)blocks * d->width * 4);
 }
 
 gs_status gs_rmsnorm_bwd(const gs_norm_desc* d, const void* s, const float* weight, const void* dy, const void* ds, void* dx,
@@ -510,7 +524,6 @@ gs_status gs_rmsnorm_bwd(const gs_norm_desc* d, const void* s, const float* weig
     const int32_t blocks = norm_blocks(d->rows, d->width);
     Carver c{static_cast<char*>(ws)};
     float* partial = static_cast<float*>(c.take((size_t)blocks * d->width * 4));
-    float* partial2 = static_cast<float*>(c.take(colsum_partial_floats(blocks, d->width) * 4));
     if (dweight) {
         st = check_ws(ws, ws_bytes, c.used);
         if (st != GS_OK) return st;
@@ -523,7 +536,7 @@ gs_status gs_rmsnorm_bwd(const gs_norm_desc* d, const void* s, const float* weig
         if (st != GS_OK) return st;
     }
     if (!dweight) return GS_OK;
-    return launched(launch_colsum(partial, GS_TYPE_F32, d->width, blocks, d->width, partial2, dweight, hs), "weight gradient");
+    return launched(launch_share_sum(ShareSum{partial, blocks, d->width, dweight}, hs), "weight gradient");
 }
 
 size_t gs_linear_workspace_size(const gs_linear_desc* d) { return forward_ws(d, false); }

@@ -185,7 +185,7 @@ __global__ __launch_bounds__(block_of(NT)) void norm_fwd_kernel(NormArgs a) {
 // The norm, backward: with n = s r, dx = ds + r (dy weight - n mean(dy weight n)), dweight = sum over rows of dy n.
 // Each group of NT threads walks rows group, group + groups, ...; its columns' share of dweight stays in
 // registers, and the shares of a workgroup's groups meet in LDS before they leave.  100000 x 256 f16: 37 us for 205 MB
-// = 5.5 TB/s, and twice 4.5 us for the sums of the shares.
+// = 5.5 TB/s, and 6 us for the sums of the shares.
 template <class T, int NT, int NC>
 __global__ __launch_bounds__(block_of(NT)) void norm_bwd_kernel(NormArgs a) {
     constexpr int RPB = rows_per_block(NT), WIDTH = NT * NC * 8;
@@ -407,9 +407,40 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(PackJobs jobs) {
 }
 
 // ---- column sums ----------------------------------------------------------------------------------
-// 64 columns x one part of the rows per workgroup: eight lanes of eight columns, 32 rows at a time, and the
-// 32 sums meet in LDS in a fixed order.  Two launches where rows are many; each is 4-5 us, the latency of its loads.
-// Atomics would save the second, but their order would change the result from run to run.
+// The sums of shares that workgroups left behind, a few thousand rows at most, in one launch: eight columns per
+// workgroup and 128 rows at a time, so that a thread's loads (16 for 2048 rows) are in flight together.  The last
+// four columns may be summed twice, in the same order, for a whole load.
+constexpr int kShareCols = 8;
+__device__ __forceinline__ void sum_shares(const ShareSum& s, int32_t block, f32x4* lds) {
+    const int x = threadIdx.x & 1, y = threadIdx.x >> 1;
+    const int32_t c0 = block * kShareCols + x * 4, c = c0 + 4 <= s.cols || s.cols < 4 ? c0 : s.cols - 4;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (c + 4 <= s.cols) {
+#pragma unroll 16
+        for (int64_t r = y; r < s.rows; r += 128) v += load_elem4(s.in, GS_TYPE_F32, r * s.cols + c);
+    } else {
+        for (int64_t r = y; r < s.rows; r += 128)
+            for (int k = 0; k < 4; k++)
+                if (c + k < s.cols) v[k] += s.in[r * s.cols + c + k];
+    }
+#pragma unroll
+    for (int m = 2; m < 64; m <<= 1)
+#pragma unroll
+        for (int k = 0; k < 4; k++) v[k] += __shfl_xor(v[k], m);
+    if ((threadIdx.x & 63) < 2) lds[(threadIdx.x >> 6) * 2 + x] = v;
+    __syncthreads();
+    if (threadIdx.x >= 2) return;
+    v = (lds[x] + lds[2 + x]) + (lds[4 + x] + lds[6 + x]);
+    for (int k = 0; k < 4; k++)
+        if (c + k < s.cols) s.out[c + k] = v[k];
+}
+__global__ __launch_bounds__(256) void share_sum_kernel(ShareSum s) {
+    __shared__ f32x4 lds[8];
+    sum_shares(s, blockIdx.x, lds);
+}
+// Rows of any type and count: 64 columns x one part of the rows per workgroup, eight lanes of eight columns, 32 rows
+// at a time, whose 32 sums meet in LDS in a fixed order; the parts are shares again.  Atomics would save the second
+// launch, but their order would change the result from run to run.
 template <class T>
 __global__ __launch_bounds__(256) void colsum_kernel(const void* in, int64_t s_row, int64_t rows, int32_t cols,
                                                      int64_t rows_per_part, float* out) {
@@ -443,26 +474,26 @@ int64_t colsum_parts(int64_t rows, int32_t cols) {
     return p < 1 ? 1 : (p > most ? most : p);
 }
 
-hipError_t launch_colsum_stage(const void* in, int type, int64_t s_row, int64_t rows, int32_t cols, int64_t parts, int64_t per,
-                               float* out, hipStream_t s) {
-    const dim3 grid((unsigned)((cols + 63) / 64), (unsigned)parts);
-    if (type == GS_TYPE_F32)
-        hipLaunchKernelGGL(colsum_kernel<F32>, grid, dim3(256), 0, s, in, s_row, rows, cols, per, out);
-    else if (type == GS_TYPE_BF16)
-        hipLaunchKernelGGL(colsum_kernel<Bf16>, grid, dim3(256), 0, s, in, s_row, rows, cols, per, out);
-    else
-        hipLaunchKernelGGL(colsum_kernel<F16>, grid, dim3(256), 0, s, in, s_row, rows, cols, per, out);
-    return hipGetLastError();
+template <class T>
+void launch_colsum_parts(const void* in, int64_t s_row, int64_t rows, int32_t cols, int64_t parts, float* out, hipStream_t s) {
+    const int64_t per = rows > 0 ? (rows + parts - 1) / parts : 1;
+    hipLaunchKernelGGL(colsum_kernel<T>, dim3((unsigned)((cols + 63) / 64), (unsigned)parts), dim3(256), 0, s, in, s_row, rows, cols,
+                       per, out);
 }
 
 // ---- join of a split product ----------------------------------------------------------------------
 // Four neighbours per group of `lanes` threads, each of which takes every lanes-th part; the parts' order is
 // fixed by the split alone.  256 parts of 256 x 64: 10 us for 17 MB, 512 of 59 x 64: 8 us for 8 MB; bound by latency.
-__global__ __launch_bounds__(256) void reduce_kernel(GemmArgs g, int lanes) {
+// The workgroups from `blocks` on add up the shares c.
+__global__ __launch_bounds__(256) void reduce_kernel(GemmArgs g, int lanes, int blocks, ShareSum c) {
     __shared__ f32x4 part[256];
+    if (blockIdx.x >= (unsigned)blocks) {
+        sum_shares(c, blockIdx.x - blocks, part);
+        return;
+    }
     const int groups = 256 / lanes, x = threadIdx.x % groups, y = threadIdx.x / groups;
     const int64_t per_row = (g.J + 3) / 4, total = per_row * g.I;
-    for (int64_t n0 = (int64_t)blockIdx.x * groups; n0 < total; n0 += (int64_t)gridDim.x * groups) {
+    for (int64_t n0 = (int64_t)blockIdx.x * groups; n0 < total; n0 += (int64_t)blocks * groups) {
         const int64_t n = n0 + x;
         const int32_t i = (int32_t)(n / per_row), j = (int32_t)(n % per_row) * 4;
         f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -559,25 +590,25 @@ hipError_t launch_pack(const void* src, int src_type, int64_t s_row, int64_t s_c
     return hipGetLastError();
 }
 
-size_t colsum_partial_floats(int64_t rows, int32_t cols) {
-    const int64_t parts = colsum_parts(rows, cols);
-    return (size_t)(parts + colsum_parts(parts, cols)) * cols;
+size_t colsum_partial_floats(int64_t rows, int32_t cols) { return (size_t)colsum_parts(rows, cols) * cols; }
+
+hipError_t launch_share_sum(const ShareSum& c, hipStream_t s) {
+    hipLaunchKernelGGL(share_sum_kernel, dim3((unsigned)((c.cols + kShareCols - 1) / kShareCols)), dim3(256), 0, s, c);
+    return hipGetLastError();
 }
 
 hipError_t launch_colsum(const void* in, int type, int64_t s_row, int64_t rows, int32_t cols, float* partial, float* out,
                          hipStream_t s) {
-    int64_t parts = colsum_parts(rows, cols);
-    const int64_t per = rows > 0 ? (rows + parts - 1) / parts : 1;
+    const int64_t parts = colsum_parts(rows, cols);
     float* to = parts > 1 ? partial : out;
-    hipError_t e = launch_colsum_stage(in, type, s_row, rows, cols, parts, per, to, s);
-    while (e == hipSuccess && parts > 1) {
-        const int64_t next = colsum_parts(parts, cols);
-        float* dst = next > 1 ? partial + parts * cols : out;
-        e = launch_colsum_stage(to, GS_TYPE_F32, cols, parts, cols, next, (parts + next - 1) / next, dst, s);
-        to = dst;
-        parts = next;
-    }
-    return e;
+    if (type == GS_TYPE_F32)
+        launch_colsum_parts<F32>(in, s_row, rows, cols, parts, to, s);
+    else if (type == GS_TYPE_BF16)
+        launch_colsum_parts<Bf16>(in, s_row, rows, cols, parts, to, s);
+    else
+        launch_colsum_parts<F16>(in, s_row, rows, cols, parts, to, s);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess && parts > 1 ? launch_share_sum(ShareSum{partial, parts, cols, out}, s) : e;
 }
 
 hipError_t launch_gemm(int type, TileShape shape, Layout la, Layout lb, EpiKind kind, const GemmArgs& g, hipStream_t s) {
@@ -592,12 +623,13 @@ hipError_t launch_few_rows(int type, EpiKind kind, const GemmArgs& g, hipStream_
     return launch_few_rows_e4m3(kind, g, s);
 }
 
-hipError_t launch_gemm_reduce(const GemmArgs& g, hipStream_t s) {
+hipError_t launch_gemm_reduce(const GemmArgs& g, const ShareSum& c, hipStream_t s) {
     const int64_t total = ((int64_t)g.J + 3) / 4 * g.I;
     const int lanes = g.splits >= 128 && total < 16384 ? 64 : g.splits >= 32 ? 16 : g.splits >= 8 ? 4 : 1;
     int64_t blocks = (total + 256 / lanes - 1) / (256 / lanes);
     if (blocks > 8192) blocks = 8192;
-    hipLaunchKernelGGL(reduce_kernel, dim3((unsigned)blocks), dim3(256), 0, s, g, lanes);
+    const int64_t more = c.out ? (c.cols + kShareCols - 1) / kShareCols : 0;
+    hipLaunchKernelGGL(reduce_kernel, dim3((unsigned)(blocks + more)), dim3(256), 0, s, g, lanes, (int)blocks, c);
     return hipGetLastError();
 }
 

@@ -327,6 +327,19 @@ def test_linear_backward(env, rows, k, n, dtype, ytype, gtype, act, bias, cm, pa
         assert abs(float((got.double() * v).sum()) - float(diff) / (2 * h)) <= (2.5 * U[dtype] + 1e-3) * float(size) + 1e-3
 
 
+@pytest.mark.parametrize("rows,act,cm", [(270_011, "none", True), (270_011, "silu", False)])
+def test_bias_gradient_of_many_rows(env, rows, act, cm):
+    """More strips of rows than one launch adds up, and a map too wide for the one-pass kernel."""
+    torch, gsmi, neural = env
+    k, n = 136, 24
+    normal, x, w, b, _, _, x64, w64, z, e_z = make_product(torch, rows, k, n, "bf16", 5, True)
+    dy = normal(*((n, rows) if cm else (rows, n)))
+    dz, e_dz = dz_bounds(torch, dy.double().t() if cm else dy.double(), z, e_z, act)
+    plan = neural.Linear(rows, k, n, torch.bfloat16, act=act, y_dtype=torch.float32, channel_major=cm,
+                         grad_dtype=torch.float32, backward=True)
+    check_grads(torch, "bf16", "f32", x64, w64, dz, e_dz, *plan.backward(x, w, dy, b))
+
+
 GATED = [  # rows, in, hidden, dtype, act, bias, pad
     (1, 1, 1, "bf16", "silu", True, 0),
     (4, 1024, 300, "bf16", "silu", False, 0),
