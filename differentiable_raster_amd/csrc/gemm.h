@@ -16,6 +16,7 @@
 
 #include "elem.h"
 #include "neural.h"
+#include "shares.h"
 
 namespace gsmi {
 namespace gemm {
@@ -374,21 +375,21 @@ __device__ __forceinline__ void tile_of(int32_t id, int32_t ni, int32_t nj, int3
 // busy for 40 %; the two gradient products of that size 478 and 545 us = 1150 and 1008 TF.
 //   Tiles of 128 (two or three per CU): the LDS reads of a step, 64 KB per 128 x 128 x 64, take as long as its
 // products.  8192 x 4096 x 1024: 75 us = 920 TF.  In 8 bits the same bytes hold twice the products at twice the rate:
-// 8192 x 1024 x 8192 gated 103 us = 1336 TF, bound by LDS and the tile's ends (8 steps a tile); a tile of 256 of that
+// 8192 x 1024 x 8192 gated 99 us = 1390 TF, bound by LDS and the tile's ends (8 steps a tile); a tile of 256 of that
 // type spills.
 //   Tiles of 64: many tiles of one or two steps, bound by memory.  59 x 64 x 1000000 onto a residual: 132 us for
 // 600 MB = 4.5 TB/s, against 5.1 of a copy.
+#ifdef __HIP_DEVICE_COMPILE__  // the host needs the kernels' names alone
 template <class T, int SHAPE, int LA, int LB, int EPI>
-__global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256, 2) void gemm_kernel(GemmArgs g) {
-#ifdef __HIP_DEVICE_COMPILE__  // the host needs the kernel's name alone
+__device__ __forceinline__ void multiply_tile(const GemmArgs& g, int32_t tile, int32_t part, char (&a0)[kTileDims[SHAPE].bi * 128],
+                                              char (&a1)[kTileDims[SHAPE].bi * 128], char (&b0)[kTileDims[SHAPE].bj * 128],
+                                              char (&b1)[kTileDims[SHAPE].bj * 128]) {
     constexpr int BI = kTileDims[SHAPE].bi, BJ = kTileDims[SHAPE].bj, WI = kTileDims[SHAPE].wi;
     constexpr int THREADS = SHAPE == kTile256 ? 512 : 256, WJ = THREADS / 64 / WI;
     constexpr int TI = BI / WI, TJ = BJ / WJ, FI = TI / 16, FJ = TJ / 16;
     constexpr bool PAIRED = EPI == kEpiGated || EPI == kEpiDGated;
     constexpr int BK = kStepBytes / (16 / T::chunk);
     constexpr int A_BYTES = BI * 128, B_BYTES = BJ * 128;
-    // objects of their own, so that the compiler knows a load into one of them does not touch the others
-    __shared__ __align__(1024) char a0[A_BYTES], a1[A_BYTES], b0[B_BYTES], b1[B_BYTES];
     typedef Operand<T, BI, THREADS, LA, false, TI> OpA;
     typedef Operand<T, BJ, THREADS, LB, PAIRED, TJ> OpB;
     constexpr int ES = OpA::ES;
@@ -397,7 +398,7 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256, 2) void gemm_kernel(
     constexpr int BJO = PAIRED ? BJ / 2 : BJ;  // result columns of a tile
     const int32_t ni = (g.I + BI - 1) / BI, nj = (g.J + BJO - 1) / BJO;
     int32_t ti, tj;
-    tile_of(blockIdx.x, ni, nj, ti, tj);
+    tile_of(tile, ni, nj, ti, tj);
     const int32_t i0 = ti * BI, j0 = tj * BJO;
 
     const char* pa = static_cast<const char*>(g.a) + (LA == kRowK ? (int64_t)i0 * g.lda : (int64_t)i0) * ES;
@@ -410,7 +411,7 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256, 2) void gemm_kernel(
     oa.init(tid, g.lda, 0);
     ob.init(tid, g.ldb, g.J);
 
-    const int32_t kt0 = (int32_t)blockIdx.z * g.kt_per_split;
+    const int32_t kt0 = part * g.kt_per_split;
     const int32_t kt_all = (int32_t)((g.K + BK - 1) / BK);
     const int32_t kt1 = kt0 + g.kt_per_split < kt_all ? kt0 + g.kt_per_split : kt_all;
 
@@ -617,8 +618,8 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256, 2) void gemm_kernel(
     float s0[8], s1[8];
 #pragma unroll
     for (int k = 0; k < 8; k++) s0[k] = s1[k] = 0.0f;
-    auto slab_rows = [&](auto part) {
-        constexpr int h = decltype(part)::value;
+    auto slab_rows = [&](auto which) {
+        constexpr int h = decltype(which)::value;
 #pragma unroll
         for (int i = 0; i < SLAB; i++)
 #pragma unroll
@@ -652,7 +653,7 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256, 2) void gemm_kernel(
                 const f32x4 a = slab[r * CPR + (c ^ (r & CM))], b = slab[r * CPR + ((c + 1) ^ (r & CM))];
                 float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
                 if (EPI == kEpiLinear && g.partial) {
-                    float* o = g.partial + ((int64_t)blockIdx.z * g.I + i) * g.J;
+                    float* o = g.partial + ((int64_t)part * g.I + i) * g.J;
                     store8(o, GS_TYPE_F32, jl, 1, g.J - jl, g.J - jl, v);
                     continue;
                 }
@@ -692,6 +693,34 @@ __global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256, 2) void gemm_kernel(
                     if (EPI == kEpiDGated) g.e.colsum[strip * cols + g.J + jl + k] = s1[k];
                 }
     }
+}
+#endif
+
+template <class T, int SHAPE, int LA, int LB, int EPI>
+__global__ __launch_bounds__(SHAPE == kTile256 ? 512 : 256, 2) void gemm_kernel(GemmArgs g) {
+#ifdef __HIP_DEVICE_COMPILE__
+    // objects of their own, so that the compiler knows a load into one of them does not touch the others
+    __shared__ __align__(1024) char a0[kTileDims[SHAPE].bi * 128], a1[kTileDims[SHAPE].bi * 128];
+    __shared__ __align__(1024) char b0[kTileDims[SHAPE].bj * 128], b1[kTileDims[SHAPE].bj * 128];
+    multiply_tile<T, SHAPE, LA, LB, EPI>(g, blockIdx.x, blockIdx.z, a0, a1, b0, b1);
+#endif
+}
+
+// The two products of a backward pass that follow dz, in tiles of 64, and the sums of the shares of dbias in one
+// launch: neither needs another's result, and the tiles of the weight gradient, which are few and long, run beside
+// those of the input's.  4099 x 1000 -> 777: 39 us, against 29 + 25 + 4.5 in three launches.
+template <class T, int SX, int SW>
+__global__ __launch_bounds__(256, 2) void gradients_kernel(GemmArgs w, int tiles_w, int blocks_w, GemmArgs x, int tiles_x,
+                                                           int blocks_x, ShareSum c) {
+#ifdef __HIP_DEVICE_COMPILE__
+    __shared__ __align__(1024) char a0[64 * 128], a1[64 * 128], b0[64 * 128], b1[64 * 128];
+    const int id = blockIdx.x;
+    if (id < blocks_w)
+        multiply_tile<T, SW, kRowFree, kRowFree, kEpiLinear>(w, id % tiles_w, id / tiles_w, a0, a1, b0, b1);
+    else if (id < blocks_w + blocks_x)
+        multiply_tile<T, SX, kRowK, kRowFree, kEpiLinear>(x, (id - blocks_w) % tiles_x, (id - blocks_w) / tiles_x, a0, a1, b0, b1);
+    else
+        sum_shares(c, id - blocks_w - blocks_x, reinterpret_cast<f32x4*>(a0));
 #endif
 }
 
@@ -703,6 +732,22 @@ hipError_t launch_one(const GemmArgs& g, hipStream_t s) {
     hipLaunchKernelGGL((gemm_kernel<T, SHAPE, LA, LB, EPI>), dim3((unsigned)tiles, 1, (unsigned)g.splits),
                        dim3(SHAPE == kTile256 ? 512 : 256), 0, s, g);
     return hipGetLastError();
+}
+
+template <class T, int SX, int SW>
+hipError_t launch_gradients_shape(const GemmArgs& w, const GemmArgs& x, const ShareSum& c, hipStream_t s) {
+    const int64_t tw = (int64_t)((w.I + 63) / 64) * ((w.J + 63) / 64), tx = (int64_t)((x.I + 63) / 64) * ((x.J + 63) / 64);
+    const int64_t blocks = tw * w.splits + tx * x.splits + (c.out ? (c.cols + kShareCols - 1) / kShareCols : 0);
+    hipLaunchKernelGGL((gradients_kernel<T, SX, SW>), dim3((unsigned)blocks), dim3(256), 0, s, w, (int)tw, (int)(tw * w.splits), x,
+                       (int)tx, (int)(tx * x.splits), c);
+    return hipGetLastError();
+}
+template <class T>
+hipError_t launch_gradients_type(TileShape sx, TileShape sw, const GemmArgs& x, const GemmArgs& w, const ShareSum& c, hipStream_t s) {
+    if (sx == kTile64 && sw == kTile64) return launch_gradients_shape<T, kTile64, kTile64>(w, x, c, s);
+    if (sx == kTile64) return launch_gradients_shape<T, kTile64, kTile64Far>(w, x, c, s);
+    if (sw == kTile64) return launch_gradients_shape<T, kTile64Far, kTile64>(w, x, c, s);
+    return launch_gradients_shape<T, kTile64Far, kTile64Far>(w, x, c, s);
 }
 
 template <class T, int SHAPE>

@@ -275,7 +275,8 @@ struct BackwardPlan {
     Tiling tz, tx, tw;
     int64_t strips;    // rows of the column sums' partials out of the z product or the copy of dy
     NarrowShape narrow;  // kp != 0: one kernel for everything
-    void *x, *w, *dz, *sums, *sums2, *partial;
+    bool together;     // dx and dweight in one launch
+    void *x, *w, *dz, *sums, *sums2, *partial, *partial_w;
     size_t bytes;
 };
 
@@ -283,6 +284,12 @@ struct BackwardPlan {
 // sums (2048 x 256: 6 us against 9), and it can go with the join of dweight (backward of 300001 x 64 -> 59: 57 us with
 // two launches of its own for dbias, 50 without).
 bool sums_at_once(const BackwardPlan& p) { return p.need_dz && p.strips <= 4096; }
+
+// Products in tiles of 64 leave the card partly idle at their start and end, and both gradients' together less
+// (backward of 4099 x 1000 -> 777: 77 us apart, 61 together).  Larger tiles are chosen where tiles fill the card.
+bool gradients_together(const Tiling& t, int64_t I, int64_t J) {
+    return (t.shape == kTile64 || t.shape == kTile64Far) && div_up(I, 64) * div_up(J, 64) * t.splits < (1 << 20);
+}
 
 BackwardPlan plan_backward(const gs_linear_desc* d, const Dims& o, bool gated, void* ws) {
     BackwardPlan p;
@@ -312,7 +319,9 @@ BackwardPlan plan_backward(const gs_linear_desc* d, const Dims& o, bool gated, v
     if (p.need_dz) p.sums = c.take((size_t)p.strips * o.n * 4);
     if (!sums_at_once(p)) p.sums2 = c.take(colsum_partial_floats(p.need_dz ? p.strips : o.m, (int32_t)o.n) * 4);
     const size_t px = p.tx.partial_bytes(o.m, o.k), pw = p.tw.partial_bytes(o.n, o.k);
-    p.partial = c.take(px > pw ? px : pw);
+    p.together = gradients_together(p.tx, o.m, o.k) && gradients_together(p.tw, o.n, o.k);
+    p.partial = c.take(p.together ? px : px > pw ? px : pw);
+    p.partial_w = p.together ? c.take(pw) : p.partial;
     p.bytes = c.used;
     return p;
 }
@@ -409,24 +418,36 @@ gs_status backward(const gs_linear_desc* d, bool gated, const void* x, const voi
     }
     const void* dz = p.need_dz ? p.dz : dy;
     const int64_t ldz = p.need_dz ? p.np : o.ld_y;
-    if (dx && o.m > 0) {
-        GemmArgs g;
-        std::memset(&g, 0, sizeof(g));
+    GemmArgs x_args, w_args;
+    std::memset(&x_args, 0, sizeof(x_args));
+    std::memset(&w_args, 0, sizeof(w_args));
+    const bool want_dx = dx && o.m > 0;
+    if (want_dx) {
+        GemmArgs& g = x_args;
         g.a = dz, g.lda = ldz, g.b = wo, g.ldb = ldw;
         g.I = d->rows, g.J = d->in, g.K = o.n, g.b_cols = (int32_t)p.kp;
         g.e.y = dx, g.e.y_si = o.ld_r, g.e.y_sj = 1, g.e.y_type = d->type;
         set_tiling(g, p.tx, p.partial);
-        e = tiled(d->type, p.tx, kRowK, kRowFree, kEpiLinear, g, s);
-        if (e != hipSuccess) return launched(e, "input gradient");
     }
     if (dweight) {
-        GemmArgs g;
-        std::memset(&g, 0, sizeof(g));
+        GemmArgs& g = w_args;
         g.a = dz, g.lda = ldz, g.b = xo, g.ldb = ldx;
         g.I = (int32_t)o.n, g.J = d->in, g.K = o.m, g.a_cols = (int32_t)p.np, g.b_cols = (int32_t)p.kp;
         g.e.y = dweight, g.e.y_si = o.k, g.e.y_sj = 1, g.e.y_type = d->grad_type;
-        set_tiling(g, p.tw, p.partial);
-        e = tiled(d->type, p.tw, kRowFree, kRowFree, kEpiLinear, g, s, shares);
+        set_tiling(g, p.tw, p.partial_w);
+    }
+    if (want_dx && dweight && p.together) {
+        e = launch_gradients(d->type, p.tx.shape, p.tw.shape, x_args, w_args, shares, s);
+        if (e == hipSuccess && x_args.partial) e = launch_gemm_reduce(x_args, kNoShares, s);
+        if (e == hipSuccess && w_args.partial) e = launch_gemm_reduce(w_args, kNoShares, s);
+        return launched(e, "gradients");
+    }
+    if (want_dx) {
+        e = tiled(d->type, p.tx, kRowK, kRowFree, kEpiLinear, x_args, s);
+        if (e != hipSuccess) return launched(e, "input gradient");
+    }
+    if (dweight) {
+        e = tiled(d->type, p.tw, kRowFree, kRowFree, kEpiLinear, w_args, s, shares);
         if (e != hipSuccess) return launched(e, "weight gradient");
     } else if (shares.out) {
         return launched(launch_share_sum(shares, s), "bias gradient");
