@@ -62,6 +62,9 @@ struct ShareSum {  // out[c] = sum_r in[r * cols + c]; out null: none
 };
 hipError_t launch_gemm_reduce(const GemmArgs& g, const ShareSum& c, hipStream_t s);
 hipError_t launch_share_sum(const ShareSum& c, hipStream_t s);
+// The join of a split projection of the backward: e as for kEpiDz, its colsum per kJoinRows rows.
+constexpr int kJoinRows = 16;
+hipError_t launch_dz_join(const GemmArgs& g, hipStream_t s);
 // Two products in one launch, x: (kRowK, kRowFree), w: (kRowFree, kRowFree), tiles kTile64 or kTile64Far, with the sums
 // of c if there are any.  Not the joins.
 hipError_t launch_gradients(int type, TileShape sx, TileShape sw, const GemmArgs& x, const GemmArgs& w, const ShareSum& c,

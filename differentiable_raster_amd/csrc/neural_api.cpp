@@ -307,12 +307,12 @@ BackwardPlan plan_backward(const gs_linear_desc* d, const Dims& o, bool gated, v
     p.need_dz = p.need_z || d->y_type != d->type || d->y_channel_major || o.n % 8 != 0 || o.ld_y % 8 != 0 || o.ld_y >= (1 << 21);
     p.kp = round8(o.k);
     p.np = round8(o.n);
-    p.tz = choose(d->type, o.m > 0 ? o.m : 1, d->out, o.k, gated, false);
+    p.tz = choose(d->type, o.m > 0 ? o.m : 1, d->out, o.k, gated, !gated);
     p.tx = choose(d->type, o.m > 0 ? o.m : 1, o.k, o.n, false, true);
     p.tw = choose(d->type, o.n, o.k, o.m, false, true);
     const TileDims td = kTileDims[p.tz.shape];
     p.few = p.need_z && use_few_rows(o, d->out, gated);
-    p.strips = p.few ? div_up(o.m, 16) : p.need_z ? div_up(o.m > 0 ? o.m : 1, td.bi) * td.wi : pack_row_blocks(o.m);
+    p.strips = p.few ? div_up(o.m, 16) : p.need_z && p.tz.splits > 1 ? div_up(o.m, kJoinRows) : p.need_z ? div_up(o.m > 0 ? o.m : 1, td.bi) * td.wi : pack_row_blocks(o.m);
     if (o.pack_x) p.x = c.take((size_t)o.m * p.kp * es);
     if (o.pack_w) p.w = c.take((size_t)o.n * p.kp * es);
     if (p.need_dz) p.dz = c.take((size_t)o.m * p.np * es);
@@ -320,7 +320,8 @@ BackwardPlan plan_backward(const gs_linear_desc* d, const Dims& o, bool gated, v
     if (!sums_at_once(p)) p.sums2 = c.take(colsum_partial_floats(p.need_dz ? p.strips : o.m, (int32_t)o.n) * 4);
     const size_t px = p.tx.partial_bytes(o.m, o.k), pw = p.tw.partial_bytes(o.n, o.k);
     p.together = gradients_together(p.tx, o.m, o.k) && gradients_together(p.tw, o.n, o.k);
-    p.partial = c.take(p.together ? px : px > pw ? px : pw);
+    const size_t pz = p.need_z && !p.few ? p.tz.partial_bytes(o.m, o.n) : 0, pg = p.together || px > pw ? px : pw;
+    p.partial = c.take(pz > pg ? pz : pg);
     p.partial_w = p.together ? c.take(pw) : p.partial;
     p.bytes = c.used;
     return p;
@@ -392,9 +393,15 @@ gs_status backward(const gs_linear_desc* d, bool gated, const void* x, const voi
         g.e.bias = bias, g.e.act = d->act;
         g.e.dy = dy, g.e.dy_type = d->y_type, g.e.d_si = d_si, g.e.d_sj = d_sj;
         g.e.colsum = dbias ? static_cast<float*>(p.sums) : nullptr;
-        set_tiling(g, p.tz, nullptr);
+        set_tiling(g, p.tz, p.partial);
         const EpiKind kind = gated ? kEpiDGated : kEpiDz;
-        e = p.few ? launch_few_rows(d->type, kind, g, s) : tiled(d->type, p.tz, kRowK, kRowK, kind, g, s);
+        if (p.few)
+            e = launch_few_rows(d->type, kind, g, s);
+        else if (p.tz.splits > 1)
+            e = launch_gemm(d->type, p.tz.shape, kRowK, kRowK, kEpiLinear, g, s);
+        else
+            e = launch_gemm(d->type, p.tz.shape, kRowK, kRowK, kind, g, s);
+        if (e == hipSuccess && !p.few && p.tz.splits > 1) e = launch_dz_join(g, s);
         if (e != hipSuccess) return launched(e, "projection of the backward");
     } else if (o.m > 0 && p.need_dz) {
         if (!cm && !dbias) {

@@ -505,7 +505,52 @@ __global__ __launch_bounds__(256) void reduce_kernel(GemmArgs g, int lanes, int 
     }
 }
 
+// The join of a split projection z of a linear map's backward: dz = dy act'(z + bias), a thread per four neighbours,
+// 16 rows x 64 columns per workgroup, and the columns' sums over those rows.  Backward of 323 x 6160 -> 64: 19 us with
+// the split, 47 without; bound by latency.
+__global__ __launch_bounds__(256) void dz_join_kernel(GemmArgs g) {
+    __shared__ float sums[kJoinRows][65];
+    const Epi& e = g.e;
+    const int x = (threadIdx.x & 15) * 4, y = threadIdx.x >> 4;
+    const int32_t i = (int32_t)blockIdx.x * kJoinRows + y, j = (int32_t)blockIdx.y * 64 + x;
+    f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (i < g.I && j < g.J) {
+        const int n = g.J - j < 4 ? g.J - j : 4;
+        const int64_t step = (int64_t)g.I * g.J, to = (int64_t)i * e.d_si + j * e.d_sj;
+        const float* p = g.partial + (int64_t)i * g.J + j;
+        f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (n == 4) {
+#pragma unroll 8
+            for (int s = 0; s < g.splits; s++) z += load_elem4(p, GS_TYPE_F32, s * step);
+        } else {
+            for (int s = 0; s < g.splits; s++)
+                for (int k = 0; k < n; k++) z[k] += p[s * step + k];
+        }
+        for (int k = 0; k < n; k++) {
+            float a, da;
+            act_both(z[k] + (e.bias ? e.bias[j + k] : 0.0f), e.act, a, da);
+            d[k] = load_elem(e.dy, e.dy_type, to + k * e.d_sj) * da;
+        }
+    }
+    // y_pad is a multiple of eight: the padding's zeros too
+    if (i < g.I && j < e.y_pad) store_elem4(e.y, e.y_type, (int64_t)i * e.y_si + j, d);
+    if (!e.colsum) return;
+    for (int k = 0; k < 4; k++) sums[y][x + k] = d[k];
+    __syncthreads();
+    const int32_t c = (int32_t)blockIdx.y * 64 + threadIdx.x;
+    if (threadIdx.x >= 64 || c >= g.J) return;
+    float t = 0.0f;
+    for (int r = 0; r < kJoinRows; r++) t += sums[r][threadIdx.x];
+    e.colsum[(int64_t)blockIdx.x * g.J + c] = t;
+}
+
 }  // namespace
+
+hipError_t launch_dz_join(const GemmArgs& g, hipStream_t s) {
+    hipLaunchKernelGGL(dz_join_kernel, dim3((unsigned)((g.I + kJoinRows - 1) / kJoinRows), (unsigned)((g.e.y_pad + 63) / 64)), dim3(256),
+                       0, s, g);
+    return hipGetLastError();
+}
 
 hipError_t launch_norm_fwd(int type, const NormArgs& a, hipStream_t s) {
     if (type == GS_TYPE_BF16) return fwd_type<Bf16>(a, s);

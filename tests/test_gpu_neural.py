@@ -298,6 +298,8 @@ LINEAR_BWD = [  # rows, in, out, dtype, y, grad, act, bias, channel_major, pad
     (4099, 32, 300, "bf16", "bf16", "f32", "none", False, False, 0),
     (20000, 48, 24, "f16", "f16", "f16", "gelu", True, False, 0),
     (300, 2048, 777, "bf16", "bf16", "bf16", "none", True, False, 0),
+    (67, 4104, 61, "f16", "f16", "f16", "silu", True, False, 0),
+    (130, 5000, 64, "bf16", "f32", "f32", "gelu", True, True, 0),
 ]
 
 
