@@ -913,7 +913,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(GemmArgs g) {
 
 // At most four rows: the matrix unit would leave three quarters of its rows empty and give a workgroup 16 rows
 // of b, which keeps most CUs idle where b has 1024 rows.  Here 64 lanes share one row of b (one gate and its up)
-// and `split` waves its summed axis, the sums are float32 multiply-adds.  1 row, 4096 -> 1024: 5.4 us for 8.4 MB, the
+// and `split` waves its summed axis, the sums are float32 multiply-adds.  1 row, 4096 -> 1024: 4.9 us for 8.4 MB, the
 // latency of a launch, one load and six exchanges between lanes; the bytes alone would be 1.7.
 template <class T>
 __device__ __forceinline__ void chunk_values(u32x4 c, float (&v)[T::chunk]) {
@@ -933,6 +933,8 @@ __device__ __forceinline__ void chunk_values(u32x4 c, float (&v)[T::chunk]) {
 }
 
 constexpr int kHandful = 4;
+// 16-byte chunks of a row whose loads a lane has in flight together
+constexpr int handful_chunks(int rows, int nb) { return rows * nb <= 2 ? 4 : 2; }
 
 template <class T, int M, int EPI>
 __global__ __launch_bounds__(256) void handful_kernel(GemmArgs g, int split) {
@@ -949,8 +951,7 @@ __global__ __launch_bounds__(256) void handful_kernel(GemmArgs g, int split) {
         const char* pb = static_cast<const char*>(g.b) + (int64_t)j * g.ldb * ES;
         const int64_t up = (int64_t)g.J * g.ldb * ES;
         const char* pa = static_cast<const char*>(g.a);
-        constexpr int U = M * NB <= 2 ? 4 : 2;  // chunks whose loads are in flight together
-        constexpr int STEP = 64 * T::chunk;
+        constexpr int U = handful_chunks(M, NB), STEP = 64 * T::chunk;
         for (int64_t k0 = (int64_t)part_k * STEP * U; k0 < g.K; k0 += (int64_t)split * STEP * U) {
             u32x4 fb[U][NB], fa[U][M];
 #pragma unroll
@@ -1013,8 +1014,11 @@ __global__ __launch_bounds__(256) void handful_kernel(GemmArgs g, int split) {
 
 template <class T, int M, int EPI>
 hipError_t launch_handful(const GemmArgs& g, hipStream_t s) {
-    // waves per column: as many waves as the card holds in one go where columns are few
-    const int split = g.J >= 1024 ? 1 : g.J >= 512 ? 2 : 4;
+    // Waves per column: as many as have a step of k each, while the launch has 4096 waves at most (1 row, 4096 -> 1024:
+    // 3.7 us with four, 4.4 with one; -> 4096: 7.9 and 6.1; 1024 -> 128: 3.3 and 3.2).
+    constexpr int STEP = 64 * T::chunk * handful_chunks(M, EPI == kEpiGated ? 2 : 1);
+    int split = 1;
+    while (split < 4 && (int64_t)STEP * split < g.K && g.J * split * 2 <= 4096) split *= 2;
     const dim3 grid((unsigned)((g.J + 4 / split - 1) / (4 / split))), block(256);
     hipLaunchKernelGGL((handful_kernel<T, M, EPI>), grid, block, 0, s, g, split);
     return hipGetLastError();
@@ -1027,16 +1031,24 @@ hipError_t launch_few_one(const GemmArgs& g, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Rows of k of more than 4 KB are where sharing them among lanes and waves pays (4 rows, 4096 -> 512: 4.4 us against 7.1
+// by matrix instructions, -> 2048: 6.7 and 7.5; but 1024 -> 512: 4.0 and 3.4); many columns fill the card anyway (4 rows,
+// 4096 -> 4096: 10 and 7.6).  One row is even where rows are short and columns up to 2048 (1024 -> 1024: 3.3 and 3.3,
+// gated 3.6 and 4.4; 1024 -> 4096: 4.2 and 3.4), and ahead where rows are long (4096 -> 4096: 6.1 and 7.2).
+template <class T>
+bool use_handful(const GemmArgs& g) {
+    const bool far = g.K * (16 / T::chunk) > 4096;
+    return g.I == 1 ? far || g.J <= 2048 : g.I <= kHandful && far && g.J <= 2048;
+}
+
 template <class T>
 hipError_t launch_few_type(EpiKind kind, const GemmArgs& g, hipStream_t s) {
     if (kind == kEpiLinear) {
-        if (g.I == 1) return launch_handful<T, 1, kEpiLinear>(g, s);
-        if (g.I <= kHandful && g.J <= 1024) return launch_handful<T, kHandful, kEpiLinear>(g, s);
+        if (use_handful<T>(g)) return g.I == 1 ? launch_handful<T, 1, kEpiLinear>(g, s) : launch_handful<T, kHandful, kEpiLinear>(g, s);
         if (g.I <= 16) return launch_few_one<T, 1, kEpiLinear>(g, s);
         if (g.I <= 32) return launch_few_one<T, 2, kEpiLinear>(g, s);
     } else if (kind == kEpiGated) {
-        if (g.I == 1) return launch_handful<T, 1, kEpiGated>(g, s);
-        if (g.I <= kHandful && g.J <= 512) return launch_handful<T, kHandful, kEpiGated>(g, s);
+        if (use_handful<T>(g)) return g.I == 1 ? launch_handful<T, 1, kEpiGated>(g, s) : launch_handful<T, kHandful, kEpiGated>(g, s);
         if (g.I <= 16) return launch_few_one<T, 1, kEpiGated>(g, s);
         if (g.I <= 32) return launch_few_one<T, 2, kEpiGated>(g, s);
     } else if constexpr (T::chunk == 8) {

@@ -139,7 +139,8 @@ gs_status check_desc(const gs_linear_desc* d, bool gated, bool backward, Dims* o
 // The kernel of few rows gives a workgroup 16 columns and all of k: where columns are few and k is long it leaves
 // most of the card idle, and the tiled product with its split wins (backward of 34 rows, 2301 -> 128: 29 us against
 // 34; but of 14 rows, 5616 -> 6112: 91 against 82).  The gated unit has no split.  From 33 rows on the tiled product
-// reads x less often (64 rows, 4096 -> 4096: 19 us against 23).  Up to four rows have a wave per column and no limit.
+// reads x less often (64 rows, 4096 -> 4096: 19 us against 23).  Up to four rows of x have no limit: long rows of the
+// weight are shared among waves there.
 bool use_few_rows(const Dims& o, int32_t out, bool gated) {
     return o.m <= 4 || (o.m <= kFewRows && (gated || out >= 1024 || o.k <= 1024));
 }

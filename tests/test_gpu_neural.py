@@ -216,6 +216,9 @@ LINEAR = [  # rows, in, out, dtype, y, act, bias, residual, channel_major, pad
     (1, 1, 1, "bf16", "bf16", "none", True, True, False, 0),
     (1, 4096, 1000, "bf16", "bf16", "none", True, True, False, 0),
     (3, 77, 130, "f16", "f16", "gelu", True, False, False, 0),
+    (2, 4104, 64, "e4m3", "bf16", "none", True, True, False, 0),
+    (4, 5000, 600, "f16", "f32", "none", True, True, True, 4),
+    (4, 2100, 2100, "bf16", "bf16", "none", False, True, False, 0),
     (16, 640, 96, "f16", "f32", "silu", False, True, False, 8),
     (17, 512, 33, "bf16", "f32", "none", True, True, True, 0),
     (33, 130, 64, "e4m3", "bf16", "relu", True, True, False, 0),
@@ -345,6 +348,9 @@ def test_bias_gradient_of_many_rows(env, rows, act, cm):
 GATED = [  # rows, in, hidden, dtype, act, bias, pad
     (1, 1, 1, "bf16", "silu", True, 0),
     (4, 1024, 300, "bf16", "silu", False, 0),
+    (3, 4104, 60, "bf16", "silu", True, 0),
+    (1, 9000, 77, "f16", "gelu", True, 3),
+    (2, 8208, 40, "e4m3", "silu", False, 0),
     (31, 77, 45, "f16", "gelu", True, 0),
     (50, 256, 96, "e4m3", "silu", True, 0),
     (65, 64, 128, "bf16", "silu", True, 0),
