@@ -107,7 +107,7 @@ constexpr int block_of(int nt) { return nt <= 64 ? 256 : nt; }
 
 // The norm, forward: r = 1 / sqrt(mean(s^2) + eps) of s = x + residual, y = s r weight.  NT threads per row, NC chunks
 // of 8 values per thread, the row in registers from its load to its last store.  16384 x 2048 bf16 with residual, sum
-// and 8-bit rows out: 43 us for 235 MB = 5.4 TB/s, a copy's rate; one row of 1024: 3.3 us, a launch.
+// and 8-bit rows out: 43 us for 235 MB = 5.4 TB/s, a copy's rate; one row of 1024: 3.0 us, a launch.
 template <class T, int NT, int NC>
 __global__ __launch_bounds__(block_of(NT)) void norm_fwd_kernel(NormArgs a) {
     __shared__ float lds[16];
